@@ -172,11 +172,16 @@ def prepare(case, seed):
 _GRID = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 
 
+def _step(e):
+    """2^e in fp32, from its bits (a power function is not exact everywhere)."""
+    return torch.where(e > -127, (e + 127) << 23, torch.full_like(e, 1 << 22)).view(torch.float32)
+
+
 def _mx_codes(x):
     """MXFP4 codes (one byte each) and E8M0 scales of x [..., K]: blocks of 32 along K."""
     b = x.float().reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
     e = (torch.frexp(b.abs().amax(-1, keepdim=True)).exponent - 3).clamp(-127, 127)
-    q = torch.ldexp(b, -e)
+    q = b / _step(e)
     m = q.abs()
     code = ((m > 0.25).to(torch.uint8) + (m >= 0.75) + (m > 1.25) + (m >= 1.75) + (m > 2.5) + (m >= 3.5) + (m > 5.0))
     code = code + 8 * torch.signbit(q).to(torch.uint8)
@@ -194,7 +199,7 @@ def _values(code, scale):
     """fp32 values of codes [..., K] (one byte each) under scales [..., K/32]."""
     grid = torch.tensor(_GRID + tuple(-v for v in _GRID), device=code.device)
     v = grid[code.int()].reshape(*code.shape[:-1], code.shape[-1] // 32, 32)
-    return torch.ldexp(v, scale.int().unsqueeze(-1) - 127).reshape(code.shape)
+    return (v * _step(scale.int().unsqueeze(-1) - 127)).reshape(code.shape)
 
 
 def _unpack(packed, scale):
@@ -311,12 +316,17 @@ def run(s):
 
 
 # ------------------------------------------------------------------ 64 bits
+def _two_to(e):
+    """2^e in fp64 for whole numbers e, from its bits."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _exact_values(packed, scale):
     """fp64 values of packed codes, from sign, exponent and mantissa bits."""
     nib = torch.stack((packed % 16, packed // 16), dim=-1).flatten(-2).long()
     exp, man = (nib // 2) % 4, (nib % 2).double()
-    mag = torch.where(exp == 0, 0.5 * man, (1 + 0.5 * man) * torch.pow(2.0, exp.double() - 1))
-    step = torch.pow(2.0, scale[..., : nib.shape[-1] // 32].double() - 127).repeat_interleave(32, dim=-1)
+    mag = torch.where(exp == 0, 0.5 * man, (1 + 0.5 * man) * _two_to(exp - 1))
+    step = _two_to(scale[..., : nib.shape[-1] // 32].long() - 127).repeat_interleave(32, dim=-1)
     return torch.where(nib >= 8, -mag, mag) * step
 
 
@@ -375,11 +385,11 @@ def exact(case, seed):
         b = (part.t().contiguous() if c["trans"] else part).double()
         b = b.reshape(b.shape[0], -1, 32)
         top = b.abs().amax(-1, keepdim=True)
-        e = torch.where(top > 0, torch.floor(torch.log2(top)) - 2, torch.full_like(top, -127.0)).clamp(-127, 127)
-        q = b / torch.pow(2.0, e)
+        e = torch.where(top > 0, torch.floor(torch.log2(top)) - 2, torch.full_like(top, -127.0)).clamp(-127, 127).long()
+        q = b / _two_to(e)
         # the nearest of the grid; of two equally near ones the even code
         d = (q.abs().unsqueeze(-1) - grid).abs() + 1e-12 * torch.arange(8, device="cuda").remainder(2)
-        v = grid[d.argmin(-1)].copysign(q) * torch.pow(2.0, e)
+        v = grid[d.argmin(-1)].copysign(q) * _two_to(e)
         values.append(v.flatten(1))
         scales.append((e + 127).to(torch.uint8).squeeze(-1))
     if not c["trans"]:
