@@ -288,6 +288,107 @@ moe_status moe_forward_noalloc(const void* x, int32_t x_dtype, int64_t T, int32_
                                float* out_f32, int32_t logits_dtype, void* logits,
                                int32_t* topk_ids, float* topk_w, void* stream);
 
+/* ------------------------------------------------------------ grouped products
+ * The experts' products on their own, with their gradients, for callers that
+ * compose or train the layer. Rows come grouped by expert: expert e has the
+ * rows [offsets[e], offsets[e + 1]) (int32 [E + 1], as moe_permute writes
+ * them: non-decreasing, any lengths, zero among them). Bounds outside [0, M]
+ * are taken as 0 or M; rows from offsets[E] on are neither read nor written.
+ * moe_grouped_gemm, for every row r of expert e:
+ *     out[r] = a[i(r)] . w[e],
+ * the input gradient of the same product being the same call with w_trans
+ * flipped. moe_grouped_wgrad, the weight gradient, for every expert:
+ *     dw[e] (+)= sum over the rows r of e of a[i(r)]^T . d[r]
+ * (an expert without rows gets zeros, or keeps what it has with accumulate).
+ * i(r) = row_index[r] / row_div, or r where row_index is NULL (row_div is then
+ * ignored): with moe_permute's sorted_pair and row_div = k the rows are
+ * gathered from the tokens. An index that is negative or from a_rows on
+ * stands for a row of zeros.
+ *   dtype     MOE_BF16, or MOE_F32 for the fp32 layer: type of a, w and d
+ *   a         [a_rows, K] (without row_index a_rows is at least M)
+ *   w         [E, K, N], or with w_trans [E, N, K]
+ *   out       [M, N] out_dtype;  d [M, N] dtype;  dw [E, K, N] out_dtype
+ * Products are exact and summed in fp32 in a fixed order (deterministic), and
+ * rounded once, to nearest even, for MOE_BF16 outputs. accumulate (0 or 1)
+ * adds to dw and needs MOE_F32 outputs. Sizes: 1 <= E <= 256, K and N
+ * multiples of 8 up to 2^20, 0 <= M < 2^29, 1 <= a_rows < 2^31, row_div >= 1. M == 0:
+ * moe_grouped_gemm does nothing, moe_grouped_wgrad writes zeros. Outputs must
+ * not overlap inputs (MOE_ERR_INVALID_ARGUMENT). No workspace. */
+moe_status moe_grouped_gemm(const void* a, int32_t dtype, int64_t a_rows, const int32_t* row_index,
+                            int32_t row_div, const void* w, int32_t w_trans, int64_t M, int32_t K,
+                            int32_t N, int32_t E, const int32_t* offsets, int32_t out_dtype,
+                            void* out, void* stream);
+moe_status moe_grouped_wgrad(const void* a, int32_t dtype, int64_t a_rows, const int32_t* row_index,
+                             int32_t row_div, const void* d, int64_t M, int32_t K, int32_t N,
+                             int32_t E, const int32_t* offsets, int32_t out_dtype,
+                             int32_t accumulate, void* dw, void* stream);
+
+/* ------------------------------------------------------------ SwiGLU and its gradient
+ * a [M, 2I] holds the gate in columns [0, I) and the up projection in [I, 2I),
+ * as moe_grouped_gemm writes them from a merged matrix. With s = 1/(1 + e^-g):
+ *   h = g * s * u
+ *   da[:, :I] = dh * u * s * (1 + g * (1 - s)),  da[:, I:] = dh * g * s
+ * in fp32, rounded once to dtype (MOE_BF16 or MOE_F32, of all arrays). The
+ * backward call forms h again if h is not NULL, so that the forward pass need
+ * not keep it. da may be a itself and h may be dh itself (in place);
+ * any other overlap returns MOE_ERR_INVALID_ARGUMENT. I a multiple of 8,
+ * 0 <= M < 2^31 (0: a no-op). */
+moe_status moe_swiglu(const void* a, int32_t dtype, int64_t M, int32_t I, void* h, void* stream);
+moe_status moe_swiglu_backward(const void* a, const void* dh, int32_t dtype, int64_t M, int32_t I,
+                               void* da, void* h, void* stream);
+
+/* ------------------------------------------------------------ finalize gradient
+ * Gradients of moe_finalize's inputs for the pairs p = t*k + j with
+ * pair_pos[p] = r >= 0, in fp32:
+ *   dy_sorted[r] = topk_w[p] * dout[t]   (dy_dtype: MOE_BF16 rounds to nearest even)
+ *   dtopk_w[p]   = sum_h dout[t, h] * y_sorted[r, h]   (fixed order)
+ * A pair without a row (negative pair_pos) gets dtopk_w 0; rows that no pair
+ * points to are left as they were. dout [T, H] dout_dtype (MOE_BF16 or
+ * MOE_F32); y_sorted [T*k, H] f32 as moe_finalize reads it; either output may
+ * be NULL (y_sorted may be NULL without dtopk_w), not both. A pair_pos from
+ * T*k on counts as negative; no two pairs may have the same row. 1 <= k <= 8,
+ * H a multiple of 64, 0 <= T < 2^24 (0: a no-op). The token
+ * gradient of the expert rows is moe_finalize itself with weights of one. */
+moe_status moe_finalize_backward(const void* dout, int32_t dout_dtype, const float* y_sorted,
+                                 const int32_t* pair_pos, const float* topk_w, int64_t T,
+                                 int32_t k, int32_t H, int32_t dy_dtype, void* dy_sorted,
+                                 float* dtopk_w, void* stream);
+
+/* ------------------------------------------------------------ MXFP4
+ * The OCP microscaling format MXFP4: blocks of 32 values along K share one
+ * E8M0 scale byte b (2^(b - 127); 255: the block is NaN), each value is an
+ * E2M1 code. Rows are K contiguous: codes [rows, K/2] (element 2j in the low
+ * nibble), scales [rows, S], S = moe_mxfp4_scale_stride(K): K/32 rounded up to
+ * a multiple of 4; the bytes past K/32 are padding (written as 127, never
+ * interpreted). K is a multiple of 32.
+ * moe_mxfp4_quantize, for each block with largest magnitude m:
+ *   scale = 2^max(floor(log2 m) - 2, -127),
+ *   code  = value / scale rounded to nearest even, magnitudes above 6 to 6
+ * (so the largest values of a block lie in [4, 6]; a block of zeros has scale
+ * byte 0; a block with an infinity or a NaN has scale byte 255 and codes 0).
+ * x is dtype (MOE_BF16 or MOE_F32): with trans = 0 [B, R, C], quantised along
+ * C into rows (B, R); with trans = 1 [B, R, C] quantised along R into rows
+ * (B, C), which turns weights stored [E, K, N] into the [E, N, K] that
+ * moe_mxfp4_grouped_gemm reads (C a multiple of 8).
+ * moe_mxfp4_dequantize writes the values of codes and scales, [R, K] dtype
+ * (exact; both types hold every value a quantised block can have). */
+int32_t moe_mxfp4_scale_stride(int32_t K);
+moe_status moe_mxfp4_quantize(const void* x, int32_t dtype, int32_t trans, int64_t B, int64_t R,
+                              int32_t C, uint8_t* codes, uint8_t* scales, void* stream);
+moe_status moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t R, int32_t K,
+                                int32_t dtype, void* out, void* stream);
+
+/* moe_grouped_gemm with both operands in MXFP4, on the fp4 MFMA:
+ *   out[r] = sum_k a[i(r), k] * w[e, :, k]
+ * a_codes, a_scales: a_rows rows of K; w_codes [E, N, K/2], w_scales [E, N, S].
+ * Rows, row_index, row_div, M and the output as moe_grouped_gemm; every product
+ * exact, sums in fp32 (fixed order). K a multiple of 32, N of 8. */
+moe_status moe_mxfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_rows,
+                                  const int32_t* row_index, int32_t row_div,
+                                  const uint8_t* w_codes, const uint8_t* w_scales, int64_t M,
+                                  int32_t K, int32_t N, int32_t E, const int32_t* offsets,
+                                  int32_t out_dtype, void* out, void* stream);
+
 /* ------------------------------------------------------------ measurement
  * Not a step of the layer: the HBM read ceiling its bandwidth-bound kernels
  * are quoted against. Reads `bytes` (a multiple of 16) of device memory at buf

@@ -29,7 +29,9 @@ ENTRY_POINTS = ("moe_status_string", "moe_route_workspace_size", "moe_route",
                 "moe_experts", "moe_experts_rows16", "moe_finalize", "moe_finalize_rows16",
                 "moe_finalize_norm", "moe_finalize_norm_rows16", "moe_forward_workspace_size",
                 "moe_forward", "moe_forward_norm", "moe_forward_noalloc",
-                "moe_hbm_read")
+                "moe_hbm_read", "moe_grouped_gemm", "moe_grouped_wgrad", "moe_swiglu",
+                "moe_swiglu_backward", "moe_finalize_backward", "moe_mxfp4_scale_stride",
+                "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_grouped_gemm")
 
 
 class MoEError(RuntimeError):
@@ -87,6 +89,19 @@ def load_library(path: str = LIB_PATH):
                                        ctypes.POINTER(CExpertWeights), _i32, _vp, _vp, _i32, _vp,
                                        _vp, _vp, _vp]),
         "moe_hbm_read": (_i32, [_vp, _sz, _vp, _vp]),
+        "moe_grouped_gemm": (_i32, [_vp, _i32, _i64, _vp, _i32, _vp, _i32, _i64, _i32, _i32, _i32,
+                                    _vp, _i32, _vp, _vp]),
+        "moe_grouped_wgrad": (_i32, [_vp, _i32, _i64, _vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp,
+                                     _i32, _i32, _vp, _vp]),
+        "moe_swiglu": (_i32, [_vp, _i32, _i64, _i32, _vp, _vp]),
+        "moe_swiglu_backward": (_i32, [_vp, _vp, _i32, _i64, _i32, _vp, _vp, _vp]),
+        "moe_finalize_backward": (_i32, [_vp, _i32, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp,
+                                         _vp]),
+        "moe_mxfp4_scale_stride": (_i32, [_i32]),
+        "moe_mxfp4_quantize": (_i32, [_vp, _i32, _i32, _i64, _i64, _i32, _vp, _vp, _vp]),
+        "moe_mxfp4_dequantize": (_i32, [_vp, _vp, _i64, _i32, _i32, _vp, _vp]),
+        "moe_mxfp4_grouped_gemm": (_i32, [_vp, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _i32, _i32,
+                                          _i32, _vp, _i32, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -297,6 +312,148 @@ def moe_forward_noalloc(x, w_router, bias, w: ExpertWeights, I: int, k: int, out
         _ptr(x), _dt(x), T, H, I, E, k, _ptr(w_router), _ptr(bias), ctypes.byref(s), _dt(out),
         _ptr(out), _ptr(out_f32), logits_dtype, _ptr(logits), _ptr(topk_ids), _ptr(topk_w),
         _stream(stream)))
+
+
+# ---------------------------------------------------------------- operators around the layer
+def _call(fn: str, tensors, stream, *args):
+    """One call of the C ABI on the tensors' own device (all on one GPU), on the
+    given stream or that device's current one."""
+    devices = {t.device for t in tensors if t is not None}
+    if any(d.type != "cuda" for d in devices):
+        raise ValueError(f"{fn} takes device tensors")
+    if len(devices) != 1:
+        raise ValueError(f"{fn}: tensors on different devices")
+    with torch.cuda.device(devices.pop()):
+        _check(fn, getattr(_lib, fn)(*args, _stream(stream)))
+
+
+def _need(fn: str, ok: bool, what: str):
+    if not ok:
+        raise ValueError(f"{fn}: {what}")
+
+
+def _rows_args(fn, M, E, offsets, row_index, row_div):
+    _need(fn, offsets.dtype == torch.int32 and offsets.shape == (E + 1,), "offsets must be int32 [E + 1]")
+    if row_index is not None:
+        _need(fn, row_index.dtype == torch.int32 and row_index.numel() == M, "row_index must be int32 [M]")
+        _need(fn, row_div >= 1, "row_div must be positive")
+
+
+def moe_grouped_gemm(a, w, offsets, out, row_index=None, row_div: int = 1, w_trans: bool = False,
+                     stream=None):
+    """out[r] = a[row_index[r] // row_div] @ w[e] for the rows r of each expert e (offsets, as
+    moe_permute writes them). a [rows, K], w [E, K, N] (w_trans: [E, N, K]), out [M, N]. The
+    input gradient is the same call on the output gradient with w_trans flipped."""
+    fn = "moe_grouped_gemm"
+    _need(fn, a.dim() == 2 and w.dim() == 3 and out.dim() == 2, "a and out are matrices, w [E, ., .]")
+    (rows, K), (M, N), E = a.shape, out.shape, w.shape[0]
+    _need(fn, tuple(w.shape[1:]) == ((N, K) if w_trans else (K, N)), "shapes of a, w and out do not match")
+    _need(fn, w.dtype == a.dtype, "a and w must have one dtype")
+    _rows_args(fn, M, E, offsets, row_index, row_div)
+    _call(fn, (a, w, offsets, out, row_index), stream, _ptr(a), _dt(a), rows, _ptr(row_index),
+          row_div, _ptr(w), int(w_trans), M, K, N, E, _ptr(offsets), _dt(out), _ptr(out))
+
+
+def moe_grouped_wgrad(a, d, offsets, dw, row_index=None, row_div: int = 1, accumulate: bool = False,
+                      stream=None):
+    """dw[e] = sum over expert e's rows r of a[row_index[r] // row_div]^T d[r] (accumulate: added
+    to dw, fp32). a [rows, K], d [M, N], dw [E, K, N]."""
+    fn = "moe_grouped_wgrad"
+    _need(fn, a.dim() == 2 and d.dim() == 2 and dw.dim() == 3, "a and d are matrices, dw [E, K, N]")
+    (rows, K), (M, N), E = a.shape, d.shape, dw.shape[0]
+    _need(fn, tuple(dw.shape[1:]) == (K, N), "shapes of a, d and dw do not match")
+    _need(fn, a.dtype == d.dtype, "a and d must have one dtype")
+    _rows_args(fn, M, E, offsets, row_index, row_div)
+    _call(fn, (a, d, offsets, dw, row_index), stream, _ptr(a), _dt(a), rows, _ptr(row_index),
+          row_div, _ptr(d), M, K, N, E, _ptr(offsets), _dt(dw), int(accumulate), _ptr(dw))
+
+
+def moe_swiglu(a, h, stream=None):
+    """h = silu(a[:, :I]) * a[:, I:]; a [M, 2I], h [M, I], bf16 or fp32."""
+    fn = "moe_swiglu"
+    _need(fn, a.dim() == 2 and tuple(a.shape) == (h.shape[0], 2 * h.shape[-1]) and h.dim() == 2,
+          "a must be [M, 2I] and h [M, I]")
+    _need(fn, a.dtype == h.dtype, "a and h must have one dtype")
+    _call(fn, (a, h), stream, _ptr(a), _dt(a), h.shape[0], h.shape[1], _ptr(h))
+
+
+def moe_swiglu_backward(a, dh, da, h=None, stream=None):
+    """da [M, 2I] = gradient of moe_swiglu at a for dh [M, I]; h [M, I], if given, is formed again.
+    da may be a and h may be dh."""
+    fn = "moe_swiglu_backward"
+    _need(fn, a.dim() == 2 and dh.dim() == 2 and tuple(a.shape) == (dh.shape[0], 2 * dh.shape[1]),
+          "a must be [M, 2I] and dh [M, I]")
+    _need(fn, da.shape == a.shape and (h is None or h.shape == dh.shape), "da is shaped as a, h as dh")
+    _need(fn, all(t is None or t.dtype == a.dtype for t in (dh, da, h)), "all tensors must have one dtype")
+    _call(fn, (a, dh, da, h), stream, _ptr(a), _ptr(dh), _dt(a), dh.shape[0], dh.shape[1], _ptr(da),
+          _ptr(h))
+
+
+def moe_finalize_backward(dout, y_sorted, pair_pos, topk_w, dy_sorted, dtopk_w, stream=None):
+    """Gradients of moe_finalize: dy_sorted[pair_pos] = topk_w * dout, dtopk_w = <dout, y_sorted[pair_pos]>
+    (either output may be None; y_sorted may be None without dtopk_w)."""
+    fn = "moe_finalize_backward"
+    _need(fn, dout.dim() == 2 and topk_w.dim() == 2, "dout must be [T, H] and topk_w [T, k]")
+    (T, H), k = dout.shape, topk_w.shape[1]
+    _need(fn, topk_w.shape[0] == T and topk_w.dtype == torch.float32, "topk_w must be fp32 [T, k]")
+    _need(fn, pair_pos.dtype == torch.int32 and pair_pos.numel() == T * k, "pair_pos must be int32 [T*k]")
+    _need(fn, y_sorted is None or (y_sorted.dtype == torch.float32 and tuple(y_sorted.shape) == (T * k, H)),
+          "y_sorted must be fp32 [T*k, H]")
+    _need(fn, dy_sorted is None or tuple(dy_sorted.shape) == (T * k, H), "dy_sorted must be [T*k, H]")
+    _need(fn, dtopk_w is None or (dtopk_w.dtype == torch.float32 and dtopk_w.shape == topk_w.shape),
+          "dtopk_w must be fp32 [T, k]")
+    _call(fn, (dout, y_sorted, pair_pos, topk_w, dy_sorted, dtopk_w), stream, _ptr(dout), _dt(dout),
+          _ptr(y_sorted), _ptr(pair_pos), _ptr(topk_w), T, k, H,
+          MOE_F32 if dy_sorted is None else _dt(dy_sorted), _ptr(dy_sorted), _ptr(dtopk_w))
+
+
+def moe_mxfp4_scale_stride(K: int) -> int:
+    """Scale bytes per row of K MXFP4 values: K / 32 rounded up to a multiple of 4."""
+    return _lib.moe_mxfp4_scale_stride(K)
+
+
+def _mx_args(fn, codes, scales, rows, K):
+    _need(fn, K % 32 == 0 and codes.dtype == torch.uint8 and tuple(codes.shape) == (*rows, K // 2),
+          "codes must be uint8 [rows, K/2], K a multiple of 32")
+    _need(fn, scales.dtype == torch.uint8 and tuple(scales.shape) == (*rows, moe_mxfp4_scale_stride(K)),
+          "scales must be uint8 [rows, moe_mxfp4_scale_stride(K)]")
+
+
+def moe_mxfp4_quantize(x, codes, scales, trans: bool = False, stream=None):
+    """MXFP4 of x [..., K] along its last dimension: codes [..., K/2], scales [..., S]. With trans,
+    x [B, K, C] (or [K, C]) along its middle dimension: codes [B, C, K/2], scales [B, C, S]."""
+    fn = "moe_mxfp4_quantize"
+    _need(fn, x.dim() in (2, 3), "x must have two or three dimensions")
+    B, R, C = x.shape if x.dim() == 3 else (1, *x.shape)
+    rows = (C,) if trans else (R,)
+    _mx_args(fn, codes, scales, (B, *rows) if x.dim() == 3 else rows, R if trans else C)
+    _call(fn, (x, codes, scales), stream, _ptr(x), _dt(x), int(trans), B, R, C, _ptr(codes), _ptr(scales))
+
+
+def moe_mxfp4_dequantize(codes, scales, out, stream=None):
+    """out [..., K] (bf16 or fp32) = the values of codes [..., K/2] under scales [..., S]."""
+    fn = "moe_mxfp4_dequantize"
+    _need(fn, out.dim() >= 1, "out must be [..., K]")
+    K = out.shape[-1]
+    _mx_args(fn, codes, scales, tuple(out.shape[:-1]), K)
+    _call(fn, (codes, scales, out), stream, _ptr(codes), _ptr(scales), out.numel() // max(K, 1), K,
+          _dt(out), _ptr(out))
+
+
+def moe_mxfp4_grouped_gemm(a_codes, a_scales, w_codes, w_scales, offsets, out, row_index=None,
+                           row_div: int = 1, stream=None):
+    """moe_grouped_gemm of MXFP4 rows a ([rows, K/2] codes, [rows, S] scales) and weights
+    ([E, N, K/2], [E, N, S]); out [M, N] bf16 or fp32."""
+    fn = "moe_mxfp4_grouped_gemm"
+    _need(fn, a_codes.dim() == 2 and w_codes.dim() == 3 and out.dim() == 2,
+          "a_codes and out are matrices, w_codes [E, N, K/2]")
+    (rows, K2), (M, N), E = a_codes.shape, out.shape, w_codes.shape[0]
+    _mx_args(fn, a_codes, a_scales, (rows,), 2 * K2)
+    _mx_args(fn, w_codes, w_scales, (E, N), 2 * K2)
+    _rows_args(fn, M, E, offsets, row_index, row_div)
+    _call(fn, (a_codes, a_scales, w_codes, w_scales, offsets, out, row_index), stream, _ptr(a_codes),
+          _ptr(a_scales), rows, _ptr(row_index), row_div, _ptr(w_codes), _ptr(w_scales), M, 2 * K2, N,
+          E, _ptr(offsets), _dt(out), _ptr(out))
 
 
 # ---------------------------------------------------------------- device plumbing
