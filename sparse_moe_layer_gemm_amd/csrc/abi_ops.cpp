@@ -77,9 +77,10 @@ moe_status moe_grouped_gemm(const void* a, int32_t dtype, int64_t a_rows, const 
     return MOE_ERR_INVALID_ARGUMENT;
   moe::GroupedArgs g{a, nullptr, a_rows, row_index, row_div, w, nullptr, (int)M, K, N, E, 0,
                      offsets, out, out_dtype == MOE_BF16, false};
-  return launch_status(moe::launch_grouped_simple(dtype == MOE_BF16 ? moe::G_BF16 : moe::G_F32,
-                                                  w_trans ? moe::G_NT : moe::G_NN, g,
-                                                  static_cast<hipStream_t>(stream)));
+  const moe::GroupedLayout lay = w_trans ? moe::G_NT : moe::G_NN;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launch_status(dtype == MOE_BF16 ? moe::launch_grouped_tile(lay, g, st)
+                                         : moe::launch_grouped_simple(moe::G_F32, lay, g, st));
 }
 
 moe_status moe_grouped_wgrad(const void* a, int32_t dtype, int64_t a_rows, const int32_t* row_index,
@@ -101,8 +102,9 @@ moe_status moe_grouped_wgrad(const void* a, int32_t dtype, int64_t a_rows, const
     return MOE_ERR_INVALID_ARGUMENT;
   moe::GroupedArgs g{a, nullptr, a_rows, row_index, row_div, d, nullptr, (int)M, K, N, E, 0,
                      offsets, dw, out_dtype == MOE_BF16, accumulate == 1};
-  return launch_status(moe::launch_grouped_simple(dtype == MOE_BF16 ? moe::G_BF16 : moe::G_F32,
-                                                  moe::G_TN, g, static_cast<hipStream_t>(stream)));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launch_status(dtype == MOE_BF16 ? moe::launch_grouped_tile(moe::G_TN, g, st)
+                                         : moe::launch_grouped_simple(moe::G_F32, moe::G_TN, g, st));
 }
 
 static moe_status check_swiglu(const void* a, int32_t dtype, int64_t M, int32_t I) {

@@ -34,6 +34,9 @@ enum GroupedInput { G_BF16 = 0, G_F32 = 1, G_MX = 2 };
 hipError_t launch_grouped_simple(GroupedInput in, GroupedLayout lay, const GroupedArgs& a,
                                  hipStream_t st);
 
+// bf16 products and weight gradients on 256 x 256 tiles.
+hipError_t launch_grouped_tile(GroupedLayout lay, const GroupedArgs& a, hipStream_t st);
+
 hipError_t launch_swiglu(const void* a, bool bf16, long long M, int I, void* h, hipStream_t st);
 hipError_t launch_swiglu_backward(const void* a, const void* dh, bool bf16, long long M, int I,
                                   void* da, void* h, hipStream_t st);
