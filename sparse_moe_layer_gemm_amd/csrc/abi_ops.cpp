@@ -227,8 +227,7 @@ moe_status moe_mxfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scale
     return MOE_ERR_INVALID_ARGUMENT;
   moe::GroupedArgs g{a_codes, a_scales, a_rows, row_index, row_div, w_codes, w_scales, (int)M, K, N,
                      E, S, offsets, out, out_dtype == MOE_BF16, false};
-  return launch_status(moe::launch_grouped_simple(moe::G_MX, moe::G_NT, g,
-                                                  static_cast<hipStream_t>(stream)));
+  return launch_status(moe::launch_mxfp4_tile(g, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

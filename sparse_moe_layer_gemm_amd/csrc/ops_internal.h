@@ -37,6 +37,9 @@ hipError_t launch_grouped_simple(GroupedInput in, GroupedLayout lay, const Group
 // bf16 products and weight gradients on 256 x 256 tiles.
 hipError_t launch_grouped_tile(GroupedLayout lay, const GroupedArgs& a, hipStream_t st);
 
+// MXFP4 products on 256 x 256 tiles of the block-scaled fp4 MFMA.
+hipError_t launch_mxfp4_tile(const GroupedArgs& a, hipStream_t st);
+
 hipError_t launch_swiglu(const void* a, bool bf16, long long M, int I, void* h, hipStream_t st);
 hipError_t launch_swiglu_backward(const void* a, const void* dh, bool bf16, long long M, int I,
                                   void* da, void* h, hipStream_t st);
