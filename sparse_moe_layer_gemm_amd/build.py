@@ -17,7 +17,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["abi.cpp", "router.hip", "permute.hip", "expert_stream.hip", "expert_stream_q.hip", "expert_tile.hip", "expert_tile_q.hip", "expert_f32.hip",
            "finalize.hip",
-           "finalize_norm.hip", "hbm_read.hip", "noalloc.hip", "abi_ops.cpp", "grouped_simple.hip", "grouped_tile.hip", "mxfp4_tile.hip",
+           "finalize_norm.hip", "hbm_read.hip", "noalloc.hip", "abi_ops.cpp", "grouped_simple.hip", "grouped_tile.hip", "grouped_stream.hip",
+           "mxfp4_tile.hip",
            "swiglu.hip", "finalize_backward.hip", "mxfp4.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -10,7 +10,7 @@ import pytest
 from sparse_moe_layer_gemm_amd import build as pkg_build
 from tests.test_asm_lds_waits_cpu import unsafe_asm_lds_reads
 
-FILES = ["grouped_tile.hip", "mxfp4_tile.hip"]
+FILES = ["grouped_tile.hip", "grouped_stream.hip", "mxfp4_tile.hip"]
 
 
 @pytest.mark.parametrize("src", FILES)
