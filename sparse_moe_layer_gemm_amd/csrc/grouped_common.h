@@ -32,6 +32,12 @@ __device__ __forceinline__ void dma16(const void* g, uint8_t* lds) {
 __device__ __forceinline__ void dma4(const void* g, uint8_t* lds) {
   __builtin_amdgcn_global_load_lds(g, (lds_void*)lds, 4, 0, 0);
 }
+// Waits until at most N of the wavefront's vector-memory operations are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt has six bits");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 // LDS reads that the compiler does not see (it would wait for every direct
 // load in flight): valid only after an lgkmcnt wait that takes them as operands.
 template <int OFF>

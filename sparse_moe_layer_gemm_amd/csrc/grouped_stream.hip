@@ -20,7 +20,7 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 enum { S_NN = 0, S_NT = 1, S_MX = 2 };
 constexpr int WAVES = 4, BN = 64;
 
-__device__ __forceinline__ int swz_row(int row) { return (row >> 2) & 3; }
+__device__ __forceinline__ int swz_row(int row) { return (row >> 2) & 2; }
 // granule g (of 8) of depth row k (128 bytes) sits at g ^ 2 f(k)
 __device__ __forceinline__ int swz_depth(int k) { return (k & 2) | ((k >> 1) & 4); }
 
@@ -143,18 +143,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void grouped_stream_kernel(GroupedAr
   for (int s = 0; s < D; ++s) issue(kb + s, s);
   int st = 0;
   for (int kt = kb; kt < ke; ++kt) {
-    static_assert((D - 1) * S::LOADS == 15 || (D - 1) * S::LOADS == 12 || (D - 1) * S::LOADS == 14 ||
-                      (D - 1) * S::LOADS == 16 || (D - 1) * S::LOADS == 21, "vmcnt literals");
-    if constexpr ((D - 1) * S::LOADS == 15)
-      asm volatile("s_waitcnt vmcnt(15)" ::: "memory");
-    else if constexpr ((D - 1) * S::LOADS == 12)
-      asm volatile("s_waitcnt vmcnt(12)" ::: "memory");
-    else if constexpr ((D - 1) * S::LOADS == 14)
-      asm volatile("s_waitcnt vmcnt(14)" ::: "memory");
-    else if constexpr ((D - 1) * S::LOADS == 16)
-      asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
-    else
-      asm volatile("s_waitcnt vmcnt(21)" ::: "memory");
+    wait_loads<(D - 1) * S::LOADS>();
     Step<KIND, RT> f;
     const uint32_t off = st * S::STAGE;
     static_for<4>([&](auto jj) {
