@@ -20,10 +20,21 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int NSTAGE = 4, OPB = 16384, SCB = 2048;  // LDS bytes of an operand's stage, of a stage's scales
-constexpr int SC0 = 2 * NSTAGE * OPB;
-constexpr int LDS_BYTES = SC0 + NSTAGE * SCB;
 constexpr int GM = 4;
+
+// Workgroup shape: 2 x WN wavefronts of up to 128 x 32 JT, NST LDS stages. The
+// scales of four steps form a chunk, two of which are in LDS.
+template <int WN_, int JT_, int NST_>
+struct Shape {
+  static constexpr int WN = WN_, JT = JT_, NST = NST_;
+  static constexpr int WAVES = 2 * WN, COLS = 32 * JT, BN = WN * COLS;
+  static constexpr int ASB = 16384, BSB = BN * 64;     // LDS bytes of an operand's stage
+  static constexpr int SC0 = NST * (ASB + BSB);        // where the scales start
+  static constexpr int SROWS = 256 + BN, SCB = SROWS * 16;
+  static constexpr int RING = SC0 + 2 * SCB;
+  static constexpr int STRIP = 128 * 2 * COLS;         // a wavefront's epilogue strip
+  static constexpr int LDS = RING > WAVES * STRIP ? RING : WAVES * STRIP;
+};
 
 __device__ __forceinline__ i32x8 widen(const u32x4& v) {
   return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
@@ -37,35 +48,35 @@ __device__ __forceinline__ f32x16 mfma_mx(const u32x4& b, uint32_t sb, const u32
 }
 __device__ __forceinline__ int swz_row(int row) { return (row >> 2) & 3; }
 
-// One half step (64 values deep): MT row and two column fragments.
-template <int MT>
+// One half step (64 values deep): MT row and JT column fragments.
+template <int MT, int JT>
 struct Half {
-  u32x4 a[MT], b[2];
+  u32x4 a[MT], b[JT];
 };
-template <int MT>
+template <int MT, int JT>
 struct Scales {
-  uint32_t a[MT], b[2];
+  uint32_t a[MT], b[JT];
 };
-template <int MT>
-__device__ __forceinline__ void wait_half(Half<MT>& f) {
+// Wait for every LDS read, of fragments or of scale dwords.
+template <class F>
+__device__ __forceinline__ void wait_reads(F& f) {
 #pragma unroll
-  for (int i = 0; i < MT; ++i) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(f.a[i])::"memory");
-  asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(f.b[0]), "+v"(f.b[1])::"memory");
-}
-template <int MT>
-__device__ __forceinline__ void wait_scales(Scales<MT>& s) {
+  for (auto& v : f.a) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(v)::"memory");
 #pragma unroll
-  for (int i = 0; i < MT; ++i) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(s.a[i])::"memory");
-  asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(s.b[0]), "+v"(s.b[1])::"memory");
+  for (auto& v : f.b) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(v)::"memory");
 }
 
 // One 64 MT x 256 tile: rows m0.. of expert e's cnt rows from lo on.
-template <int MT>
+template <class S, bool S16, int MT>
 __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int e, int lo, int cnt,
                                         int m0, int n0) {
-  constexpr int QA = MT == 4 ? 2 : 1, LOADS = QA + 3;
+  constexpr int JT = S::JT, NST = S::NST;
+  constexpr int NA = 4 * MT, QA = NA / S::WAVES > 0 ? NA / S::WAVES : 1, QB = S::BN / 16 / S::WAVES;
+  constexpr int LOADS = QA + QB;
+  // rows of scales a wavefront loads: one per lane and load
+  constexpr int QS = (S::SROWS / 64 + S::WAVES - 1) / S::WAVES;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / S::WN, wn = wave % S::WN;
   const int rb = g.K / 2, nb = g.K / 32;  // bytes and blocks per row
   const int nk = (g.K + 127) >> 7;
   const char* const zeros = reinterpret_cast<const char*>(kZeros);
@@ -74,226 +85,266 @@ __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int
 
   // ---- direct loads: instruction q fills 16 rows, lane p physical granule
   // p % 4 of row p / 4; lim = steps for which the lane's granule lies inside K
-  const char *ap[2], *bp[2], *sp;
-  int alim[2], blim[2], slim;
+  const char *ap[QA], *bp[QB], *sp[QS];
+  int alim[QA], blim[QB], slim[QS];
 #pragma unroll
   for (int q = 0; q < QA; ++q) {
-    const int row = 16 * ((wave * QA + q) & (4 * MT - 1)) + (lane >> 2);
+    const int row = 16 * ((wave * QA + q) & (NA - 1)) + (lane >> 2);
     const int lg = (lane & 3) ^ swz_row(row);
     const int s = m0 + row < cnt ? source_row(g, lo + m0 + row) : -1;
     ap[q] = A + (size_t)(s < 0 ? 0 : s) * rb + 16 * lg;
     alim[q] = s < 0 ? 0 : (rb - 16 * lg + 63) >> 6;
   }
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int row = 16 * (wave * 2 + q) + (lane >> 2);
+  for (int q = 0; q < QB; ++q) {
+    const int row = 16 * (wave * QB + q) + (lane >> 2);
     const int lg = (lane & 3) ^ swz_row(row);
     const bool ok = n0 + row < g.N;
     bp[q] = W + ((size_t)e * g.N + (ok ? n0 + row : 0)) * rb + 16 * lg;
     blim[q] = ok ? (rb - 16 * lg + 63) >> 6 : 0;
   }
-  // scales: one row per lane, wavefronts 0-3 those of a, 4-7 those of w
-  if (wave < 4) {
-    const int row = 64 * wave + lane;
-    const int s = (row < 64 * MT && m0 + row < cnt) ? source_row(g, lo + m0 + row) : -1;
-    sp = reinterpret_cast<const char*>(g.a_scale) + (size_t)(s < 0 ? 0 : s) * g.S;
-    slim = s < 0 ? 0 : nk;
-  } else {
-    const int row = 64 * (wave - 4) + lane;
-    const bool ok = n0 + row < g.N;
-    sp = reinterpret_cast<const char*>(g.w_scale) + ((size_t)e * g.N + (ok ? n0 + row : 0)) * g.S;
-    slim = ok ? nk : 0;
+  // scales: rows 0-255 those of a, then those of w; the last rows once more where
+  // the loads do not divide. slim = bytes of the row
+#pragma unroll
+  for (int q = 0; q < QS; ++q) {
+    const int blk = min(wave * QS + q, S::SROWS / 64 - 1), row = 64 * blk + lane;
+    if (blk < 4) {
+      const int s = (row < 64 * MT && m0 + row < cnt) ? source_row(g, lo + m0 + row) : -1;
+      sp[q] = reinterpret_cast<const char*>(g.a_scale) + (size_t)(s < 0 ? 0 : s) * g.S;
+      slim[q] = s < 0 ? 0 : g.S;
+    } else {
+      const bool ok = n0 + row - 256 < g.N;
+      sp[q] = reinterpret_cast<const char*>(g.w_scale) + ((size_t)e * g.N + (ok ? n0 + row - 256 : 0)) * g.S;
+      slim[q] = ok ? g.S : 0;
+    }
   }
-  auto issue = [&](int kt, int st) {
-    uint8_t* As = smem + st * OPB;
-    uint8_t* Bs = smem + (NSTAGE + st) * OPB;
+  // Loads of step kt; with the first of four steps (chunk), first of all, their scales:
+  // 16 bytes a row where rows are whole 16-byte groups (S16), else four
+  // dwords, which land as four planes of one dword per row.
+  auto issue = [&](int kt, int st, bool chunk) {
+    uint8_t* As = smem + st * S::ASB;
+    uint8_t* Bs = smem + NST * S::ASB + st * S::BSB;
+    if (chunk) {
+#pragma unroll
+      for (int q = 0; q < QS; ++q) {
+        const int blk = min(wave * QS + q, S::SROWS / 64 - 1);
+        uint8_t* p = smem + S::SC0 + ((kt >> 2) & 1) * S::SCB;
+        if constexpr (S16) {
+          dma16(4 * kt < slim[q] ? sp[q] + 4 * kt : zeros, p + blk * 1024);
+        } else {
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            dma4(4 * (kt + d) < slim[q] ? sp[q] + 4 * (kt + d) : zeros, p + (d * S::SROWS + blk * 64) * 4);
+        }
+      }
+    }
 #pragma unroll
     for (int q = 0; q < QA; ++q)
       dma16(kt < alim[q] ? ap[q] + (size_t)kt * 64 : zeros,
-            As + ((wave * QA + q) & (4 * MT - 1)) * 1024);
+            As + ((wave * QA + q) & (NA - 1)) * 1024);
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-      dma16(kt < blim[q] ? bp[q] + (size_t)kt * 64 : zeros, Bs + (wave * 2 + q) * 1024);
-    dma4(kt < slim ? sp + 4 * kt : zeros, smem + SC0 + st * SCB + wave * 256);
+    for (int q = 0; q < QB; ++q)
+      dma16(kt < blim[q] ? bp[q] + (size_t)kt * 64 : zeros, Bs + (wave * QB + q) * 1024);
   };
 
   // ---- fragments
   const int l32 = lane & 31, kh = lane >> 5;
   const uint32_t lds0 = (uint32_t)(size_t)(lds_u8*)smem;
-  const int am = wm * 32 * MT, bn = wn * 64;
+  const int am = wm * 32 * MT, bn = wn * S::COLS;
   uint32_t aaddr[2], baddr[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int gr = ((2 * kh + s) ^ swz_row(l32)) << 4;
     aaddr[s] = lds0 + (am + l32) * 64 + gr;
-    baddr[s] = lds0 + NSTAGE * OPB + (bn + l32) * 64 + gr;
+    baddr[s] = lds0 + NST * S::ASB + (bn + l32) * 64 + gr;
   }
-  const uint32_t saddr = lds0 + SC0 + (am + l32) * 4, sbddr = lds0 + SC0 + 1024 + (bn + l32) * 4;
-  auto load_half = [&](Half<MT>& f, int st, int s) {
-    static_for<2>([&](auto j) {
-      f.b[decltype(j)::value] = lds_b128<decltype(j)::value * 2048>(baddr[s] + st * OPB);
+  // scale dword of a row: 16 bytes a row, or a plane per step of the chunk
+  constexpr int SROW = S16 ? 16 : 4;
+  const uint32_t saddr = lds0 + S::SC0 + (am + l32) * SROW, sbddr = lds0 + S::SC0 + (256 + bn + l32) * SROW;
+  // the stage (step % 4) is a compile-time constant: every read has an immediate offset
+  auto load_half = [&](Half<MT, JT>& f, auto stage, auto half) {
+    constexpr int st = decltype(stage)::value, s = decltype(half)::value;
+    static_for<JT>([&](auto j) {
+      f.b[decltype(j)::value] = lds_b128<st * S::BSB + decltype(j)::value * 2048>(baddr[s]);
     });
     static_for<MT>([&](auto i) {
-      f.a[decltype(i)::value] = lds_b128<decltype(i)::value * 2048>(aaddr[s] + st * OPB);
+      f.a[decltype(i)::value] = lds_b128<st * S::ASB + decltype(i)::value * 2048>(aaddr[s]);
     });
   };
-  auto load_scales = [&](Scales<MT>& f, int st) {
-    static_for<2>([&](auto j) {
-      f.b[decltype(j)::value] = lds_b32<decltype(j)::value * 128>(sbddr + st * SCB);
+  auto load_scales = [&](Scales<MT, JT>& f, auto stage, int chunk) {
+    constexpr int at = decltype(stage)::value * (S16 ? 4 : 4 * S::SROWS);
+    const uint32_t off = (chunk & 1) * S::SCB;
+    static_for<JT>([&](auto j) {
+      f.b[decltype(j)::value] = lds_b32<at + decltype(j)::value * 32 * SROW>(sbddr + off);
     });
     static_for<MT>([&](auto i) {
-      f.a[decltype(i)::value] = lds_b32<decltype(i)::value * 128>(saddr + st * SCB);
+      f.a[decltype(i)::value] = lds_b32<at + decltype(i)::value * 32 * SROW>(saddr + off);
     });
   };
   // this lane's two scale bytes of step kt, in the low half; bytes past K / 32 are zero
-  auto cut = [&](Scales<MT>& f, int kt) {
+  auto cut = [&](Scales<MT, JT>& f, int kt) {
     const int left = nb - 4 * kt - 2 * kh;
     const uint32_t width = left >= 2 ? 16u : left == 1 ? 8u : 0u;
 #pragma unroll
     for (int i = 0; i < MT; ++i) f.a[i] = __builtin_amdgcn_ubfe(f.a[i], 16 * kh, width);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) f.b[j] = __builtin_amdgcn_ubfe(f.b[j], 16 * kh, width);
+    for (int j = 0; j < JT; ++j) f.b[j] = __builtin_amdgcn_ubfe(f.b[j], 16 * kh, width);
   };
 
-  f32x16 acc[MT][2];
+  f32x16 acc[MT][JT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < JT; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  auto mfmas = [&](const Half<MT>& f, const Scales<MT>& s, auto half) {
-    constexpr int S = decltype(half)::value;
+  auto mfmas = [&](const Half<MT, JT>& f, const Scales<MT, JT>& s, auto half) {
+    constexpr int H = decltype(half)::value;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mfma_mx<S>(f.b[j], s.b[j], f.a[i], s.a[i], acc[i][j]);
+      for (int j = 0; j < JT; ++j) acc[i][j] = mfma_mx<H>(f.b[j], s.b[j], f.a[i], s.a[i], acc[i][j]);
   };
   constexpr std::integral_constant<int, 0> first{};
   constexpr std::integral_constant<int, 1> second{};
 
 #pragma unroll
-  for (int s = 0; s < NSTAGE; ++s) issue(s, s);
-  if constexpr (LOADS == 5)
-    asm volatile("s_waitcnt vmcnt(15)" ::: "memory");
-  else
-    asm volatile("s_waitcnt vmcnt(12)" ::: "memory");
+  for (int s = 0; s < NST; ++s) issue(s, s, s == 0);
+  // the first step has landed (scale loads in flight only make the wait stricter)
+  wait_loads<(NST - 1) * LOADS>();
   __builtin_amdgcn_s_barrier();
-  Half<MT> f0, f1;
-  Scales<MT> s0, s1;
-  auto step = [&](int kt, Scales<MT>& sc, Scales<MT>& scn) {
-    const int st = kt & (NSTAGE - 1), sn = (kt + 1) & (NSTAGE - 1);
-    load_half(f1, st, 1);
+  Half<MT, JT> f0, f1;
+  Scales<MT, JT> s0, s1;
+  auto step = [&](auto stage, int kt, Scales<MT, JT>& sc, Scales<MT, JT>& scn) {
+    constexpr int st = decltype(stage)::value;
+    constexpr std::integral_constant<int, (st + 1) % NST> next{};
+    load_half(f1, stage, second);
     mfmas(f0, sc, first);
-    wait_half(f1);
+    wait_reads(f1);
     // everyone has read this stage after the barrier, and the next one has landed
-    if constexpr (LOADS == 5)
-      asm volatile("s_waitcnt vmcnt(10)" ::: "memory");
-    else
-      asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    wait_loads<(NST - 2) * LOADS>();
     __builtin_amdgcn_s_barrier();
-    issue(kt + NSTAGE, st);
-    load_scales(scn, sn);
-    load_half(f0, sn, 0);
+    issue(kt + NST, st, st == 0);
+    load_scales(scn, next, (kt + 1) >> 2);
+    load_half(f0, next, first);
     mfmas(f1, sc, second);
-    wait_scales(scn);
-    wait_half(f0);
+    wait_reads(scn);
+    wait_reads(f0);
     cut(scn, kt + 1);
   };
-  load_scales(s0, 0);
-  load_half(f0, 0, 0);
-  wait_scales(s0);
-  wait_half(f0);
+  load_scales(s0, first, 0);
+  load_half(f0, first, first);
+  wait_reads(s0);
+  wait_reads(f0);
   cut(s0, 0);
-  // two steps at a time (an odd depth ends with a step of zeros): the scales
-  // alternate between two register sets without copies
-  for (int kt = 0; kt < nk; kt += 2) {
-    step(kt, s0, s1);
-    step(kt + 1, s1, s0);
+  // four steps per turn (a depth of other than whole turns ends with steps of
+  // zeros); the scales alternate between two register sets without copies
+  static_assert(NST == 4, "four steps per turn of the loop");
+  for (int kt = 0; kt < nk; kt += 4) {
+    step(std::integral_constant<int, 0>{}, kt, s0, s1);
+    step(std::integral_constant<int, 1>{}, kt + 1, s1, s0);
+    step(std::integral_constant<int, 2>{}, kt + 2, s0, s1);
+    step(std::integral_constant<int, 3>{}, kt + 3, s1, s0);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
 
-  // ---- epilogue: lane l holds rows 32 i + l % 32, columns 32 j + 8 q + 4 (l / 32) + 0..3
-  uint8_t* strip = smem + wave * 16384;
-  if (g.out_bf16) {
-    // 32 MT rows of 128 bytes; granule c of row r at c ^ (r >> 1 & 7)
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int r = 32 * i + l32, c = 4 * j + q;
-          const f32x16& v = acc[i][j];
-          *reinterpret_cast<u32x2*>(strip + r * 128 + ((c ^ ((r >> 1) & 7)) << 4) + 8 * kh) =
-              u32x2{bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3])};
-        }
+  // ---- epilogue: lane l holds rows 32 i + l % 32, columns 32 j + 8 q + 4 (l / 32) + 0..3,
+  // through the wavefront's strip of LDS so that a row's columns leave together;
+  // the 16-byte granules are swizzled by row
+  uint8_t* strip = smem + wave * S::STRIP;
+  auto fence = [] {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+  if (g.out_bf16) {
+    constexpr int GR = S::COLS / 8;  // granules per row
+    auto at = [&](int r, int c) { return strip + r * (2 * S::COLS) + ((c ^ ((GR == 8 ? r >> 1 : r) & 7)) << 4); };
 #pragma unroll
-    for (int t = 0; t < 4 * MT; ++t) {
-      const int r = 8 * t + (lane >> 3), c = lane & 7;
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < JT; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& v = acc[i][j];
+          *reinterpret_cast<u32x2*>(at(32 * i + l32, 4 * j + q) + 8 * kh) =
+              u32x2{bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3])};
+        }
+    fence();
+#pragma unroll
+    for (int t = 0; t < 32 * MT * GR / 64; ++t) {
+      const int r = (64 / GR) * t + lane / GR, c = lane % GR;
       const int m = m0 + am + r, n = n0 + bn + 8 * c;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(strip + r * 128 + ((c ^ ((r >> 1) & 7)) << 4));
+      const u32x4 v = *reinterpret_cast<const u32x4*>(at(r, c));
       if (m < cnt && n < g.N)
         *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.out) + ((size_t)lo + m) * g.N + n) = v;
     }
   } else {
-    // fp32: 64 rows at a time, rows of 256 bytes; granule c of row r at c ^ (r & 15)
-    constexpr int R = MT < 2 ? 1 : 2;
+    // fp32: 64 rows at a time
+    constexpr int GR = S::COLS / 4, R = MT < 2 ? 1 : 2;
+    auto at = [&](int r, int c) { return strip + r * (4 * S::COLS) + ((c ^ (r & 15)) << 4); };
     static_for<MT / R>([&](auto hh) {
       constexpr int h = decltype(hh)::value;
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < JT; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int r = 32 * i + l32, c = 8 * j + 2 * q + kh;
             const f32x16& v = acc[R * h + i][j];
-            *reinterpret_cast<f32x4*>(strip + r * 256 + ((c ^ (r & 15)) << 4)) =
+            *reinterpret_cast<f32x4*>(at(32 * i + l32, 8 * j + 2 * q + kh)) =
                 f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
           }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      fence();
 #pragma unroll
-      for (int t = 0; t < 8 * R; ++t) {
-        const int r = 4 * t + (lane >> 4), c = lane & 15;
+      for (int t = 0; t < 32 * R * GR / 64; ++t) {
+        const int r = (64 / GR) * t + lane / GR, c = lane % GR;
         const int m = m0 + am + 32 * R * h + r, n = n0 + bn + 4 * c;
-        const f32x4 v = *reinterpret_cast<const f32x4*>(strip + r * 256 + ((c ^ (r & 15)) << 4));
+        const f32x4 v = *reinterpret_cast<const f32x4*>(at(r, c));
         if (m < cnt && n < g.N)
           *reinterpret_cast<f32x4*>(static_cast<float*>(g.out) + ((size_t)lo + m) * g.N + n) = v;
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      fence();
     });
   }
 }
 
-__global__ __launch_bounds__(512, 1) void mxfp4_tile_kernel(GroupedArgs g, int nt) {
-  __shared__ __align__(1024) uint8_t smem[LDS_BYTES];
+template <class S, bool S16>
+__global__ __launch_bounds__(64 * S::WAVES, S::WAVES == 4 && S::JT == 2 ? 2 : 1) void mxfp4_tile_kernel(
+    GroupedArgs g, int nt) {
+  __shared__ __align__(1024) uint8_t smem[S::LDS];
   RowTile t;
   if (!find_tile<256, GM>(g, nt, t)) return;
-  const int left = t.cnt - t.m0;
+  const int left = t.cnt - t.m0, n0 = S::BN * t.nt;
   if (left > 128)
-    mx_body<4>(g, smem, t.e, t.lo, t.cnt, t.m0, 256 * t.nt);
+    mx_body<S, S16, 4>(g, smem, t.e, t.lo, t.cnt, t.m0, n0);
   else if (left > 64)
-    mx_body<2>(g, smem, t.e, t.lo, t.cnt, t.m0, 256 * t.nt);
+    mx_body<S, S16, 2>(g, smem, t.e, t.lo, t.cnt, t.m0, n0);
   else
-    mx_body<1>(g, smem, t.e, t.lo, t.cnt, t.m0, 256 * t.nt);
+    mx_body<S, S16, 1>(g, smem, t.e, t.lo, t.cnt, t.m0, n0);
 }
+
+#ifndef SHV
+#define SHV 0
+#endif
+#if SHV == 0
+using Big = Shape<4, 2, 4>;
+#else
+using Big = Shape<2, 4, 4>;
+#endif
 
 }  // namespace
 
 hipError_t launch_mxfp4_tile(const GroupedArgs& a, hipStream_t st) {
-  const int nt = (a.N + 255) / 256;
+  using S = Big;
+  const int nt = (a.N + S::BN - 1) / S::BN, lanes = 64 * S::WAVES;
   const long long n = (max_row_tiles(a.M, a.E, 256) * nt + 7) / 8 * 8;
-  if (n * 512 >= (1LL << 32)) return hipErrorInvalidValue;
-  mxfp4_tile_kernel<<<(unsigned)n, 512, 0, st>>>(a, nt);
+  if (n * lanes >= (1LL << 32)) return hipErrorInvalidValue;
+  if (a.S % 16 == 0)
+    mxfp4_tile_kernel<S, true><<<(unsigned)n, lanes, 0, st>>>(a, nt);
+  else
+    mxfp4_tile_kernel<S, false><<<(unsigned)n, lanes, 0, st>>>(a, nt);
   return hipGetLastError();
 }
 
