@@ -32,6 +32,19 @@ __device__ __forceinline__ void dma16(const void* g, uint8_t* lds) {
 __device__ __forceinline__ void dma4(const void* g, uint8_t* lds) {
   __builtin_amdgcn_global_load_lds(g, (lds_void*)lds, 4, 0, 0);
 }
+// The same through a buffer of `bytes` bytes at base: offsets from there on read
+// zeros. kOut + (anything below 2^20) is such an offset in a buffer of at most kOut bytes.
+constexpr uint32_t kOut = 0xFFF00000u;
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer make_buffer(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ void dma16(Buffer b, uint32_t off, uint8_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)lds, 16, (int)off, 0, 0, 0);
+}
+__device__ __forceinline__ void dma4(Buffer b, uint32_t off, uint8_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)lds, 4, (int)off, 0, 0, 0);
+}
 // Waits until at most N of the wavefront's vector-memory operations are in flight.
 template <int N>
 __device__ __forceinline__ void wait_loads() {

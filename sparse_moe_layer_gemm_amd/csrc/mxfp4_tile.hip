@@ -22,19 +22,14 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int GM = 4;
 
-// Workgroup shape: 2 x WN wavefronts of up to 128 x 32 JT, NST LDS stages. The
-// scales of four steps form a chunk, two of which are in LDS.
-template <int WN_, int JT_, int NST_>
-struct Shape {
-  static constexpr int WN = WN_, JT = JT_, NST = NST_;
-  static constexpr int WAVES = 2 * WN, COLS = 32 * JT, BN = WN * COLS;
-  static constexpr int ASB = 16384, BSB = BN * 64;     // LDS bytes of an operand's stage
-  static constexpr int SC0 = NST * (ASB + BSB);        // where the scales start
-  static constexpr int SROWS = 256 + BN, SCB = SROWS * 16;
-  static constexpr int RING = SC0 + 2 * SCB;
-  static constexpr int STRIP = 128 * 2 * COLS;         // a wavefront's epilogue strip
-  static constexpr int LDS = RING > WAVES * STRIP ? RING : WAVES * STRIP;
-};
+// Workgroup: 2 x 4 wavefronts of up to 128 x 64. A stage holds 128 bytes (256
+// values) of 256 rows of each operand; the scales of four stages form a chunk.
+constexpr int WN = 4, JT = 2, WAVES = 2 * WN, COLS = 32 * JT, BN = WN * COLS, NST = 2;
+constexpr int OPB = 256 * 128, SROWS = 256 + BN, SCB = SROWS * 32;
+constexpr int SC0 = 2 * NST * OPB;          // where the scales start
+constexpr int STRIP = 128 * 2 * COLS;       // a wavefront's epilogue strip
+constexpr int LDS_BYTES = SC0 + 2 * SCB;
+static_assert(WAVES * STRIP <= LDS_BYTES && LDS_BYTES <= 160 * 1024, "LDS");
 
 __device__ __forceinline__ i32x8 widen(const u32x4& v) {
   return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
@@ -46,14 +41,16 @@ __device__ __forceinline__ f32x16 mfma_mx(const u32x4& b, uint32_t sb, const u32
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(b), widen(a), c, 4, 4, S, (int)sb, S,
                                                          (int)sa);
 }
-__device__ __forceinline__ int swz_row(int row) { return (row >> 2) & 3; }
+// granule g (of 8) of row r sits at g ^ swz_row(r): the 16 rows that ds_read_b128
+// serves together (lanes 0-3, 12-15, 20-27, and so on) cover all banks
+__device__ __forceinline__ int swz_row(int row) { return (row >> 1) & 7; }
 
-// One half step (64 values deep): MT row and JT column fragments.
-template <int MT, int JT>
-struct Half {
+// A quarter of a stage (64 values deep): MT row and JT column fragments.
+template <int MT>
+struct Quarter {
   u32x4 a[MT], b[JT];
 };
-template <int MT, int JT>
+template <int MT>
 struct Scales {
   uint32_t a[MT], b[JT];
 };
@@ -67,128 +64,130 @@ __device__ __forceinline__ void wait_reads(F& f) {
 }
 
 // One 64 MT x 256 tile: rows m0.. of expert e's cnt rows from lo on.
-template <class S, bool S16, int MT>
+template <bool S16, bool BIG, int MT>
 __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int e, int lo, int cnt,
                                         int m0, int n0) {
-  constexpr int JT = S::JT, NST = S::NST;
-  constexpr int NA = 4 * MT, QA = NA / S::WAVES > 0 ? NA / S::WAVES : 1, QB = S::BN / 16 / S::WAVES;
-  constexpr int LOADS = QA + QB;
-  // rows of scales a wavefront loads: one per lane and load
-  constexpr int QS = (S::SROWS / 64 + S::WAVES - 1) / S::WAVES;
+  // 1 KB loads (8 rows of 128 bytes) per wavefront and stage
+  constexpr int QA = MT, QB = BN / 8 / WAVES, LOADS = QA + QB;
+  constexpr int QS = SROWS / 64 / WAVES;  // blocks of 64 rows whose scales a wavefront loads
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int wm = wave / WN, wn = wave % WN;
   const int rb = g.K / 2, nb = g.K / 32;  // bytes and blocks per row
-  const int nk = (g.K + 127) >> 7;
+  const int nd = (g.K + 255) >> 8;        // stages
   const char* const zeros = reinterpret_cast<const char*>(kZeros);
-  const char* A = static_cast<const char*>(g.a);
-  const char* W = static_cast<const char*>(g.w);
+  const char* const A = static_cast<const char*>(g.a);
+  const char* const W = static_cast<const char*>(g.w);
 
-  // ---- direct loads: instruction q fills 16 rows, lane p physical granule
-  // p % 4 of row p / 4; lim = steps for which the lane's granule lies inside K
-  const char *ap[QA], *bp[QB], *sp[QS];
-  int alim[QA], blim[QB], slim[QS];
+  // ---- direct loads: lane p holds physical granule p % 8 of row p / 8. Rows of
+  // a that are none, and its granules past K, read zeros; w reads past its row
+  // there (every code is a finite number, and meets a's zero), and zeros past its
+  // last row. BIG: a passes the 32 bits of a buffer offset and is addressed in 64.
+  int arow[QA], ag[2];  // source rows (-1: none) or their bytes; bytes of the granule, by row parity
+  uint32_t brow[QB];
 #pragma unroll
   for (int q = 0; q < QA; ++q) {
-    const int row = 16 * ((wave * QA + q) & (NA - 1)) + (lane >> 2);
-    const int lg = (lane & 3) ^ swz_row(row);
-    const int s = m0 + row < cnt ? source_row(g, lo + m0 + row) : -1;
-    ap[q] = A + (size_t)(s < 0 ? 0 : s) * rb + 16 * lg;
-    alim[q] = s < 0 ? 0 : (rb - 16 * lg + 63) >> 6;
+    const int row = 8 * (wave * QA + q) + (lane >> 3);
+    const int r = m0 + row < cnt ? source_row(g, lo + m0 + row) : -1;
+    arow[q] = BIG ? r : (int)(r < 0 ? kOut : (uint32_t)r * (uint32_t)rb);
   }
 #pragma unroll
-  for (int q = 0; q < QB; ++q) {
-    const int row = 16 * (wave * QB + q) + (lane >> 2);
-    const int lg = (lane & 3) ^ swz_row(row);
-    const bool ok = n0 + row < g.N;
-    bp[q] = W + ((size_t)e * g.N + (ok ? n0 + row : 0)) * rb + 16 * lg;
-    blim[q] = ok ? (rb - 16 * lg + 63) >> 6 : 0;
+  for (int q = 0; q < QB; ++q) brow[q] = (uint32_t)(8 * (wave * QB + q) + (lane >> 3)) * (uint32_t)rb;
+  const int wrows = min(BN, g.N - n0);
+  const Buffer wbuf = make_buffer(W + ((size_t)e * g.N + n0) * rb, (uint32_t)wrows * (uint32_t)rb);
+  const Buffer abuf = make_buffer(A, BIG ? 0u : (uint32_t)g.a_rows * (uint32_t)rb);
+  // swz_row(8 x + y) = (4 x + y / 2) % 8: two granules a lane, for even and odd x
+#pragma unroll
+  for (int x = 0; x < 2; ++x) ag[x] = 16 * ((lane & 7) ^ swz_row(8 * x + (lane >> 3)));
+  // Scales: rows 0-255 those of a (wavefronts 0-3), then those of w. S16 (rows of
+  // whole 16-byte groups): 32 bytes a row per chunk, two lanes a row, two loads
+  // per block of 64 rows; else a row per lane and eight dword loads, which land
+  // as eight planes of one dword per row. Bytes past a row's scales are cut below.
+  constexpr int QR = S16 ? 2 * QS : QS;
+  static_assert(64 * QS * 4 == 256, "wavefronts 0-3 load a's scales");
+  uint32_t srow[QR];
+#pragma unroll
+  for (int q = 0; q < QR; ++q) {
+    const int row = S16 ? 64 * QS * (wave & 3) + 32 * q + (lane >> 1) : 64 * (QS * (wave & 3) + q) + lane;
+    int r = row;
+    if (wave < 4) r = (row < 64 * MT && m0 + row < cnt) ? source_row(g, lo + m0 + row) : -1;
+    srow[q] = (r < 0 ? kOut : (uint32_t)r * (uint32_t)g.S) + (S16 ? 16 * (lane & 1) : 0);
   }
-  // scales: rows 0-255 those of a, then those of w; the last rows once more where
-  // the loads do not divide. slim = bytes of the row
+  const Buffer sbuf = wave < 4 ? make_buffer(g.a_scale, (uint32_t)g.a_rows * (uint32_t)g.S)
+                               : make_buffer(g.w_scale + ((size_t)e * g.N + n0) * g.S, (uint32_t)wrows * (uint32_t)g.S);
+  auto issue_scales = [&](int d) {  // the chunk that starts with stage d
+    uint8_t* p = smem + SC0 + ((d >> 2) & 1) * SCB;
 #pragma unroll
-  for (int q = 0; q < QS; ++q) {
-    const int blk = min(wave * QS + q, S::SROWS / 64 - 1), row = 64 * blk + lane;
-    if (blk < 4) {
-      const int s = (row < 64 * MT && m0 + row < cnt) ? source_row(g, lo + m0 + row) : -1;
-      sp[q] = reinterpret_cast<const char*>(g.a_scale) + (size_t)(s < 0 ? 0 : s) * g.S;
-      slim[q] = s < 0 ? 0 : g.S;
-    } else {
-      const bool ok = n0 + row - 256 < g.N;
-      sp[q] = reinterpret_cast<const char*>(g.w_scale) + ((size_t)e * g.N + (ok ? n0 + row - 256 : 0)) * g.S;
-      slim[q] = ok ? g.S : 0;
-    }
-  }
-  // Loads of step kt; with the first of four steps (chunk), first of all, their scales:
-  // 16 bytes a row where rows are whole 16-byte groups (S16), else four
-  // dwords, which land as four planes of one dword per row.
-  auto issue = [&](int kt, int st, bool chunk) {
-    uint8_t* As = smem + st * S::ASB;
-    uint8_t* Bs = smem + NST * S::ASB + st * S::BSB;
-    if (chunk) {
+    for (int q = 0; q < QR; ++q) {
+      if constexpr (S16) {
+        dma16(sbuf, srow[q] + 8 * d, p + (64 * QS * wave + 32 * q) * 32);
+      } else {
 #pragma unroll
-      for (int q = 0; q < QS; ++q) {
-        const int blk = min(wave * QS + q, S::SROWS / 64 - 1);
-        uint8_t* p = smem + S::SC0 + ((kt >> 2) & 1) * S::SCB;
-        if constexpr (S16) {
-          dma16(4 * kt < slim[q] ? sp[q] + 4 * kt : zeros, p + blk * 1024);
-        } else {
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-            dma4(4 * (kt + d) < slim[q] ? sp[q] + 4 * (kt + d) : zeros, p + (d * S::SROWS + blk * 64) * 4);
-        }
+        for (int x = 0; x < 8; ++x)
+          dma4(sbuf, srow[q] + 8 * d + 4 * x, p + (x * SROWS + 64 * (QS * wave + q)) * 4);
       }
     }
+  };
+  auto issue = [&](int d, int st) {
+    uint8_t* As = smem + st * OPB;
+    uint8_t* Bs = smem + (NST + st) * OPB;
+    int at[2];
 #pragma unroll
-    for (int q = 0; q < QA; ++q)
-      dma16(kt < alim[q] ? ap[q] + (size_t)kt * 64 : zeros,
-            As + ((wave * QA + q) & (NA - 1)) * 1024);
+    for (int x = 0; x < 2; ++x) at[x] = ag[x] + 128 * d;
+#pragma unroll
+    for (int q = 0; q < QA; ++q) {
+      const int o = QA % 2 ? ((wave & 1) ? at[1] : at[0]) : at[q & 1];
+      uint8_t* p = As + (wave * QA + q) * 1024;
+      if constexpr (BIG)
+        dma16(arow[q] >= 0 && o < rb ? A + ((size_t)arow[q] * rb + o) : zeros, p);
+      else
+        dma16(abuf, o < rb ? (uint32_t)arow[q] + (uint32_t)o : kOut, p);
+    }
 #pragma unroll
     for (int q = 0; q < QB; ++q)
-      dma16(kt < blim[q] ? bp[q] + (size_t)kt * 64 : zeros, Bs + (wave * QB + q) * 1024);
+      dma16(wbuf, brow[q] + (uint32_t)at[q & 1], Bs + (wave * QB + q) * 1024);
   };
 
-  // ---- fragments
+  // ---- fragments: of a stage's eight granules lanes 0-31 take 0-3, the others
+  // 4-7, so that a lane's four scale bytes of a stage are one dword
   const int l32 = lane & 31, kh = lane >> 5;
   const uint32_t lds0 = (uint32_t)(size_t)(lds_u8*)smem;
-  const int am = wm * 32 * MT, bn = wn * S::COLS;
-  uint32_t aaddr[2], baddr[2];
+  const int am = wm * 32 * MT, bn = wn * COLS;
+  uint32_t aaddr[4], baddr[4];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int gr = ((2 * kh + s) ^ swz_row(l32)) << 4;
-    aaddr[s] = lds0 + (am + l32) * 64 + gr;
-    baddr[s] = lds0 + NST * S::ASB + (bn + l32) * 64 + gr;
+  for (int h = 0; h < 4; ++h) {
+    const int gr = ((4 * kh + h) ^ swz_row(l32)) << 4;
+    aaddr[h] = lds0 + (am + l32) * 128 + gr;
+    baddr[h] = lds0 + NST * OPB + (bn + l32) * 128 + gr;
   }
-  // scale dword of a row: 16 bytes a row, or a plane per step of the chunk
-  constexpr int SROW = S16 ? 16 : 4;
-  const uint32_t saddr = lds0 + S::SC0 + (am + l32) * SROW, sbddr = lds0 + S::SC0 + (256 + bn + l32) * SROW;
-  // the stage (step % 4) is a compile-time constant: every read has an immediate offset
-  auto load_half = [&](Half<MT, JT>& f, auto stage, auto half) {
-    constexpr int st = decltype(stage)::value, s = decltype(half)::value;
+  constexpr int SROW = S16 ? 32 : 4, SKH = S16 ? 4 : 4 * SROWS;
+  const uint32_t saddr = lds0 + SC0 + (am + l32) * SROW + kh * SKH,
+                 sbddr = lds0 + SC0 + (256 + bn + l32) * SROW + kh * SKH;
+  auto load_quarter = [&](Quarter<MT>& f, auto stage, auto quarter) {
+    constexpr int st = decltype(stage)::value, h = decltype(quarter)::value;
     static_for<JT>([&](auto j) {
-      f.b[decltype(j)::value] = lds_b128<st * S::BSB + decltype(j)::value * 2048>(baddr[s]);
+      f.b[decltype(j)::value] = lds_b128<st * OPB + decltype(j)::value * 4096>(baddr[h]);
     });
     static_for<MT>([&](auto i) {
-      f.a[decltype(i)::value] = lds_b128<st * S::ASB + decltype(i)::value * 2048>(aaddr[s]);
+      f.a[decltype(i)::value] = lds_b128<st * OPB + decltype(i)::value * 4096>(aaddr[h]);
     });
   };
-  auto load_scales = [&](Scales<MT, JT>& f, auto stage, int chunk) {
-    constexpr int at = decltype(stage)::value * (S16 ? 4 : 4 * S::SROWS);
-    const uint32_t off = (chunk & 1) * S::SCB;
+  auto load_scales = [&](Scales<MT>& f, int d) {
+    const uint32_t off = ((d >> 2) & 1) * SCB + (d & 3) * 2 * SKH;
     static_for<JT>([&](auto j) {
-      f.b[decltype(j)::value] = lds_b32<at + decltype(j)::value * 32 * SROW>(sbddr + off);
+      f.b[decltype(j)::value] = lds_b32<decltype(j)::value * 32 * SROW>(sbddr + off);
     });
     static_for<MT>([&](auto i) {
-      f.a[decltype(i)::value] = lds_b32<at + decltype(i)::value * 32 * SROW>(saddr + off);
+      f.a[decltype(i)::value] = lds_b32<decltype(i)::value * 32 * SROW>(saddr + off);
     });
   };
-  // this lane's two scale bytes of step kt, in the low half; bytes past K / 32 are zero
-  auto cut = [&](Scales<MT, JT>& f, int kt) {
-    const int left = nb - 4 * kt - 2 * kh;
-    const uint32_t width = left >= 2 ? 16u : left == 1 ? 8u : 0u;
+  // scale bytes past K / 32 are no scales: zero (their codes are zeros)
+  auto cut = [&](Scales<MT>& f, int d) {
+    const int left = nb - 8 * d - 4 * kh;
+    const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : 0xFFFFFFFFu >> (32 - 8 * left);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) f.a[i] = __builtin_amdgcn_ubfe(f.a[i], 16 * kh, width);
+    for (int i = 0; i < MT; ++i) f.a[i] &= keep;
 #pragma unroll
-    for (int j = 0; j < JT; ++j) f.b[j] = __builtin_amdgcn_ubfe(f.b[j], 16 * kh, width);
+    for (int j = 0; j < JT; ++j) f.b[j] &= keep;
   };
 
   f32x16 acc[MT][JT];
@@ -198,69 +197,76 @@ __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int
     for (int j = 0; j < JT; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  auto mfmas = [&](const Half<MT, JT>& f, const Scales<MT, JT>& s, auto half) {
-    constexpr int H = decltype(half)::value;
+  auto mfmas = [&](const Quarter<MT>& f, const Scales<MT>& s, auto quarter) {
+    constexpr int H = decltype(quarter)::value;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int j = 0; j < JT; ++j) acc[i][j] = mfma_mx<H>(f.b[j], s.b[j], f.a[i], s.a[i], acc[i][j]);
   };
-  constexpr std::integral_constant<int, 0> first{};
-  constexpr std::integral_constant<int, 1> second{};
+  constexpr std::integral_constant<int, 0> c0{};
+  constexpr std::integral_constant<int, 1> c1{};
+  constexpr std::integral_constant<int, 2> c2{};
+  constexpr std::integral_constant<int, 3> c3{};
 
-#pragma unroll
-  for (int s = 0; s < NST; ++s) issue(s, s, s == 0);
-  // the first step has landed (scale loads in flight only make the wait stricter)
-  wait_loads<(NST - 1) * LOADS>();
+  issue_scales(0);
+  issue(0, 0);
+  issue(1, 1);
+  wait_loads<LOADS>();
   __builtin_amdgcn_s_barrier();
-  Half<MT, JT> f0, f1;
-  Scales<MT, JT> s0, s1;
-  auto step = [&](auto stage, int kt, Scales<MT, JT>& sc, Scales<MT, JT>& scn) {
-    constexpr int st = decltype(stage)::value;
-    constexpr std::integral_constant<int, (st + 1) % NST> next{};
-    load_half(f1, stage, second);
-    mfmas(f0, sc, first);
+  Quarter<MT> f0, f1;
+  Scales<MT> s0, s1;
+  // stage d: its first quarter is in f0, its scales in sc
+  auto stage = [&](auto st, int d, Scales<MT>& sc, Scales<MT>& scn) {
+    constexpr std::integral_constant<int, 1 - decltype(st)::value> next{};
+    load_quarter(f1, st, c1);
+    mfmas(f0, sc, c0);
+    wait_reads(f1);
+    load_quarter(f0, st, c2);
+    mfmas(f1, sc, c1);
+    wait_reads(f0);
+    load_quarter(f1, st, c3);
+    mfmas(f0, sc, c2);
     wait_reads(f1);
     // everyone has read this stage after the barrier, and the next one has landed
-    wait_loads<(NST - 2) * LOADS>();
+    wait_loads<0>();
     __builtin_amdgcn_s_barrier();
-    issue(kt + NST, st, st == 0);
-    load_scales(scn, next, (kt + 1) >> 2);
-    load_half(f0, next, first);
-    mfmas(f1, sc, second);
+    if constexpr (decltype(st)::value == 0)
+      if ((d & 2) != 0) issue_scales(d + 2);
+    issue(d + 2, decltype(st)::value);
+    load_scales(scn, d + 1);
+    load_quarter(f0, next, c0);
+    mfmas(f1, sc, c3);
     wait_reads(scn);
     wait_reads(f0);
-    cut(scn, kt + 1);
+    cut(scn, d + 1);
   };
-  load_scales(s0, first, 0);
-  load_half(f0, first, first);
+  load_scales(s0, 0);
+  load_quarter(f0, c0, c0);
   wait_reads(s0);
   wait_reads(f0);
   cut(s0, 0);
-  // four steps per turn (a depth of other than whole turns ends with steps of
-  // zeros); the scales alternate between two register sets without copies
-  static_assert(NST == 4, "four steps per turn of the loop");
-  for (int kt = 0; kt < nk; kt += 4) {
-    step(std::integral_constant<int, 0>{}, kt, s0, s1);
-    step(std::integral_constant<int, 1>{}, kt + 1, s1, s0);
-    step(std::integral_constant<int, 2>{}, kt + 2, s0, s1);
-    step(std::integral_constant<int, 3>{}, kt + 3, s1, s0);
+  // two stages per turn (an odd number ends with one of zeros): the scales
+  // alternate between two register sets without copies
+  for (int d = 0; d < nd; d += 2) {
+    stage(c0, d, s0, s1);
+    stage(c1, d + 1, s1, s0);
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  wait_loads<0>();
   __builtin_amdgcn_s_barrier();
 
   // ---- epilogue: lane l holds rows 32 i + l % 32, columns 32 j + 8 q + 4 (l / 32) + 0..3,
   // through the wavefront's strip of LDS so that a row's columns leave together;
   // the 16-byte granules are swizzled by row
-  uint8_t* strip = smem + wave * S::STRIP;
+  uint8_t* strip = smem + wave * STRIP;
   auto fence = [] {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   };
   if (g.out_bf16) {
-    constexpr int GR = S::COLS / 8;  // granules per row
-    auto at = [&](int r, int c) { return strip + r * (2 * S::COLS) + ((c ^ ((GR == 8 ? r >> 1 : r) & 7)) << 4); };
+    constexpr int GR = COLS / 8;  // granules per row
+    auto at = [&](int r, int c) { return strip + r * (2 * COLS) + ((c ^ ((GR == 8 ? r >> 1 : r) & 7)) << 4); };
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -282,8 +288,8 @@ __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int
     }
   } else {
     // fp32: 64 rows at a time
-    constexpr int GR = S::COLS / 4, R = MT < 2 ? 1 : 2;
-    auto at = [&](int r, int c) { return strip + r * (4 * S::COLS) + ((c ^ (r & 15)) << 4); };
+    constexpr int GR = COLS / 4, R = MT < 2 ? 1 : 2;
+    auto at = [&](int r, int c) { return strip + r * (4 * COLS) + ((c ^ (r & 15)) << 4); };
     static_for<MT / R>([&](auto hh) {
       constexpr int h = decltype(hh)::value;
 #pragma unroll
@@ -310,41 +316,33 @@ __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int
   }
 }
 
-template <class S, bool S16>
-__global__ __launch_bounds__(64 * S::WAVES, S::WAVES == 4 && S::JT == 2 ? 2 : 1) void mxfp4_tile_kernel(
-    GroupedArgs g, int nt) {
-  __shared__ __align__(1024) uint8_t smem[S::LDS];
+template <bool S16, bool BIG>
+__global__ __launch_bounds__(64 * WAVES, 1) void mxfp4_tile_kernel(GroupedArgs g, int nt) {
+  __shared__ __align__(1024) uint8_t smem[LDS_BYTES];
   RowTile t;
   if (!find_tile<256, GM>(g, nt, t)) return;
-  const int left = t.cnt - t.m0, n0 = S::BN * t.nt;
+  const int left = t.cnt - t.m0, n0 = BN * t.nt;
   if (left > 128)
-    mx_body<S, S16, 4>(g, smem, t.e, t.lo, t.cnt, t.m0, n0);
+    mx_body<S16, BIG, 4>(g, smem, t.e, t.lo, t.cnt, t.m0, n0);
   else if (left > 64)
-    mx_body<S, S16, 2>(g, smem, t.e, t.lo, t.cnt, t.m0, n0);
+    mx_body<S16, BIG, 2>(g, smem, t.e, t.lo, t.cnt, t.m0, n0);
   else
-    mx_body<S, S16, 1>(g, smem, t.e, t.lo, t.cnt, t.m0, n0);
+    mx_body<S16, BIG, 1>(g, smem, t.e, t.lo, t.cnt, t.m0, n0);
 }
-
-#ifndef SHV
-#define SHV 0
-#endif
-#if SHV == 0
-using Big = Shape<4, 2, 4>;
-#else
-using Big = Shape<2, 4, 4>;
-#endif
 
 }  // namespace
 
 hipError_t launch_mxfp4_tile(const GroupedArgs& a, hipStream_t st) {
-  using S = Big;
-  const int nt = (a.N + S::BN - 1) / S::BN, lanes = 64 * S::WAVES;
+  const int nt = (a.N + BN - 1) / BN, lanes = 64 * WAVES;
   const long long n = (max_row_tiles(a.M, a.E, 256) * nt + 7) / 8 * 8;
   if (n * lanes >= (1LL << 32)) return hipErrorInvalidValue;
-  if (a.S % 16 == 0)
-    mxfp4_tile_kernel<S, true><<<(unsigned)n, lanes, 0, st>>>(a, nt);
+  // buffer offsets have 32 bits, and the codes are the larger part of a
+  if (a.a_rows * (a.K / 2) > (long long)kOut)
+    mxfp4_tile_kernel<false, true><<<(unsigned)n, lanes, 0, st>>>(a, nt);
+  else if (a.S % 16 == 0)
+    mxfp4_tile_kernel<true, false><<<(unsigned)n, lanes, 0, st>>>(a, nt);
   else
-    mxfp4_tile_kernel<S, false><<<(unsigned)n, lanes, 0, st>>>(a, nt);
+    mxfp4_tile_kernel<false, false><<<(unsigned)n, lanes, 0, st>>>(a, nt);
   return hipGetLastError();
 }
 
