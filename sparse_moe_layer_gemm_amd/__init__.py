@@ -345,7 +345,8 @@ def _need(fn: str, ok: bool, what: str):
 
 
 def _rows_args(fn, M, E, offsets, row_index, row_div):
-    _need(fn, offsets.dtype == torch.int32 and offsets.shape == (E + 1,), "offsets must be int32 [E + 1]")
+    if offsets.dtype != torch.int32 or offsets.shape != (E + 1,):
+        raise ValueError(f"{fn}: offsets must be int32 [E + 1]")
     if row_index is not None:
         _need(fn, row_index.dtype == torch.int32 and row_index.numel() == M, "row_index must be int32 [M]")
         _need(fn, row_div >= 1, "row_div must be positive")
@@ -359,7 +360,7 @@ def moe_grouped_gemm(a, w, offsets, out, row_index=None, row_div: int = 1, w_tra
     fn = "moe_grouped_gemm"
     _need(fn, a.dim() == 2 and w.dim() == 3 and out.dim() == 2, "a and out are matrices, w [E, ., .]")
     (rows, K), (M, N), E = a.shape, out.shape, w.shape[0]
-    _need(fn, tuple(w.shape[1:]) == ((N, K) if w_trans else (K, N)), "shapes of a, w and out do not match")
+    _need(fn, w.shape[1:] == ((N, K) if w_trans else (K, N)), "shapes of a, w and out do not match")
     _need(fn, w.dtype == a.dtype, "a and w must have one dtype")
     _rows_args(fn, M, E, offsets, row_index, row_div)
     _call(fn, (a, w, offsets, out, row_index), stream, _ptr(a), _dt(a), rows, _ptr(row_index),
@@ -373,7 +374,7 @@ def moe_grouped_wgrad(a, d, offsets, dw, row_index=None, row_div: int = 1, accum
     fn = "moe_grouped_wgrad"
     _need(fn, a.dim() == 2 and d.dim() == 2 and dw.dim() == 3, "a and d are matrices, dw [E, K, N]")
     (rows, K), (M, N), E = a.shape, d.shape, dw.shape[0]
-    _need(fn, tuple(dw.shape[1:]) == (K, N), "shapes of a, d and dw do not match")
+    _need(fn, dw.shape[1:] == (K, N), "shapes of a, d and dw do not match")
     _need(fn, a.dtype == d.dtype, "a and d must have one dtype")
     _rows_args(fn, M, E, offsets, row_index, row_div)
     _call(fn, (a, d, offsets, dw, row_index), stream, _ptr(a), _dt(a), rows, _ptr(row_index),
@@ -383,7 +384,7 @@ def moe_grouped_wgrad(a, d, offsets, dw, row_index=None, row_div: int = 1, accum
 def moe_swiglu(a, h, stream=None):
     """h = silu(a[:, :I]) * a[:, I:]; a [M, 2I], h [M, I], bf16 or fp32."""
     fn = "moe_swiglu"
-    _need(fn, a.dim() == 2 and tuple(a.shape) == (h.shape[0], 2 * h.shape[-1]) and h.dim() == 2,
+    _need(fn, h.dim() == 2 and a.shape == (h.shape[0], 2 * h.shape[1]),
           "a must be [M, 2I] and h [M, I]")
     _need(fn, a.dtype == h.dtype, "a and h must have one dtype")
     _call(fn, (a, h), stream, _ptr(a), _dt(a), h.shape[0], h.shape[1], _ptr(h))
@@ -393,7 +394,7 @@ def moe_swiglu_backward(a, dh, da, h=None, stream=None):
     """da [M, 2I] = gradient of moe_swiglu at a for dh [M, I]; h [M, I], if given, is formed again.
     da may be a and h may be dh."""
     fn = "moe_swiglu_backward"
-    _need(fn, a.dim() == 2 and dh.dim() == 2 and tuple(a.shape) == (dh.shape[0], 2 * dh.shape[1]),
+    _need(fn, dh.dim() == 2 and a.shape == (dh.shape[0], 2 * dh.shape[1]),
           "a must be [M, 2I] and dh [M, I]")
     _need(fn, da.shape == a.shape and (h is None or h.shape == dh.shape), "da is shaped as a, h as dh")
     _need(fn, all(t is None or t.dtype == a.dtype for t in (dh, da, h)), "all tensors must have one dtype")
@@ -409,9 +410,9 @@ def moe_finalize_backward(dout, y_sorted, pair_pos, topk_w, dy_sorted, dtopk_w, 
     (T, H), k = dout.shape, topk_w.shape[1]
     _need(fn, topk_w.shape[0] == T and topk_w.dtype == torch.float32, "topk_w must be fp32 [T, k]")
     _need(fn, pair_pos.dtype == torch.int32 and pair_pos.numel() == T * k, "pair_pos must be int32 [T*k]")
-    _need(fn, y_sorted is None or (y_sorted.dtype == torch.float32 and tuple(y_sorted.shape) == (T * k, H)),
+    _need(fn, y_sorted is None or (y_sorted.dtype == torch.float32 and y_sorted.shape == (T * k, H)),
           "y_sorted must be fp32 [T*k, H]")
-    _need(fn, dy_sorted is None or tuple(dy_sorted.shape) == (T * k, H), "dy_sorted must be [T*k, H]")
+    _need(fn, dy_sorted is None or dy_sorted.shape == (T * k, H), "dy_sorted must be [T*k, H]")
     _need(fn, dtopk_w is None or (dtopk_w.dtype == torch.float32 and dtopk_w.shape == topk_w.shape),
           "dtopk_w must be fp32 [T, k]")
     _call(fn, (dout, y_sorted, pair_pos, topk_w, dy_sorted, dtopk_w), stream, _ptr(dout), _dt(dout),
@@ -425,10 +426,10 @@ def moe_mxfp4_scale_stride(K: int) -> int:
 
 
 def _mx_args(fn, codes, scales, rows, K):
-    _need(fn, K % 32 == 0 and codes.dtype == torch.uint8 and tuple(codes.shape) == (*rows, K // 2),
-          "codes must be uint8 [rows, K/2], K a multiple of 32")
-    _need(fn, scales.dtype == torch.uint8 and tuple(scales.shape) == (*rows, moe_mxfp4_scale_stride(K)),
-          "scales must be uint8 [rows, moe_mxfp4_scale_stride(K)]")
+    if K % 32 != 0 or codes.dtype != torch.uint8 or codes.shape != (*rows, K // 2):
+        raise ValueError(f"{fn}: codes must be uint8 [rows, K/2], K a multiple of 32")
+    if scales.dtype != torch.uint8 or scales.shape != (*rows, (K // 32 + 3) // 4 * 4):
+        raise ValueError(f"{fn}: scales must be uint8 [rows, moe_mxfp4_scale_stride(K)]")
 
 
 def moe_mxfp4_quantize(x, codes, scales, trans: bool = False, stream=None):
@@ -447,7 +448,7 @@ def moe_mxfp4_dequantize(codes, scales, out, stream=None):
     fn = "moe_mxfp4_dequantize"
     _need(fn, out.dim() >= 1, "out must be [..., K]")
     K = out.shape[-1]
-    _mx_args(fn, codes, scales, tuple(out.shape[:-1]), K)
+    _mx_args(fn, codes, scales, out.shape[:-1], K)
     _call(fn, (codes, scales, out), stream, _ptr(codes), _ptr(scales), out.numel() // max(K, 1), K,
           _dt(out), _ptr(out))
 

@@ -1,32 +1,34 @@
 // Gradient of the weighted un-permute out[t] = sum_j w[t, j] y[pos[t, j]]:
 //   dy[pos[t, j]] = w[t, j] dout[t],   dw[t, j] = <dout[t], y[pos[t, j]]>.
 //
-// One workgroup per token reads dout[t] once and the token's k rows of y once,
-// and writes k rows of dy: HBM-bound (y fp32 dominates). A lane takes 8
-// adjacent columns and issues the loads of all k slots together; the k dots
-// are summed per lane over its columns, then over the wavefront (butterfly)
-// and the workgroup's wavefronts in order, so results are deterministic.
+// A workgroup takes SL slots of a token: it reads dout[t] and the slots' rows of
+// y once and writes their rows of dy, so it is HBM-bound (y fp32 dominates). A
+// lane takes 8 adjacent columns and issues the loads of all its slots together;
+// the dots are summed per lane over its columns, then over the wavefront
+// (butterfly) and the workgroup's wavefronts in order, so results are
+// deterministic and do not depend on SL.
 #include "ops_common.h"
 
 namespace moe {
 namespace {
 
-template <bool DOUT_BF16, bool DY_BF16>
+template <bool DOUT_BF16, bool DY_BF16, int SL, bool NT>
 __global__ __launch_bounds__(1024) void finalize_backward_kernel(
     const void* __restrict__ dout, const float* __restrict__ y, const int32_t* __restrict__ pos,
     const float* __restrict__ w, int T, int k, int H, void* __restrict__ dy,
     float* __restrict__ dw) {
-  __shared__ float part[16][8];
+  __shared__ float part[16][SL];
   const int tid = threadIdx.x;
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    const long long p0 = (long long)t * k;
-    long long row[8];
-    float wj[8], dot[8];
+    const int j0 = SL * blockIdx.y, nj = min(k - j0, SL);
+    const long long p0 = (long long)t * k + j0;
+    long long row[SL];
+    float wj[SL], dot[SL];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      row[j] = j < k ? pos[p0 + j] : -1;
+    for (int j = 0; j < SL; ++j) {
+      row[j] = j < nj ? pos[p0 + j] : -1;
       if (row[j] >= (long long)T * k) row[j] = -1;
-      wj[j] = j < k ? w[p0 + j] : 0.f;
+      wj[j] = j < nj ? w[p0 + j] : 0.f;
       dot[j] = 0.f;
     }
     for (int c = 8 * tid; c < H; c += 8 * blockDim.x) {
@@ -44,16 +46,16 @@ __global__ __launch_bounds__(1024) void finalize_backward_kernel(
         for (int i = 0; i < 4; ++i) d[i] = a[i], d[4 + i] = b[i];
       }
       if (dw) {
-        f32x4 v[8][2];
+        f32x4 v[SL][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < SL; ++j)
           if (row[j] >= 0) {
             const f32x4* q = reinterpret_cast<const f32x4*>(y + row[j] * H + c);
-            v[j][0] = __builtin_nontemporal_load(q);
-            v[j][1] = __builtin_nontemporal_load(q + 1);
+            v[j][0] = *q;
+            v[j][1] = q[1];
           }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < SL; ++j)
           if (row[j] >= 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) dot[j] = fmaf(d[i], v[j][0][i], dot[j]);
@@ -63,13 +65,13 @@ __global__ __launch_bounds__(1024) void finalize_backward_kernel(
       }
       if (dy) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < SL; ++j)
           if (row[j] >= 0) {
             if constexpr (DY_BF16) {
               u32x4 o;
 #pragma unroll
               for (int i = 0; i < 4; ++i) o[i] = bf16_pair(wj[j] * d[2 * i], wj[j] * d[2 * i + 1]);
-              *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(dy) + row[j] * H + c) = o;
+              store_once<NT>(reinterpret_cast<u32x4*>(static_cast<uint16_t*>(dy) + row[j] * H + c), o);
             } else {
               f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(dy) + row[j] * H + c);
               q[0] = f32x4{wj[j] * d[0], wj[j] * d[1], wj[j] * d[2], wj[j] * d[3]};
@@ -80,13 +82,13 @@ __global__ __launch_bounds__(1024) void finalize_backward_kernel(
     }
     if (!dw) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dot[j] = wave_sum(dot[j]);
+    for (int j = 0; j < SL; ++j) dot[j] = wave_sum(dot[j]);
     if ((tid & 63) == 0) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) part[tid >> 6][j] = dot[j];
+      for (int j = 0; j < SL; ++j) part[tid >> 6][j] = dot[j];
     }
     __syncthreads();
-    if (tid < k) {
+    if (tid < nj) {
       float s = 0.f;
       for (int q = 0; q < (int)(blockDim.x >> 6); ++q) s += part[q][tid];
       dw[p0 + tid] = s;
@@ -105,20 +107,34 @@ hipError_t launch_finalize_backward(const void* dout, bool dout_bf16, const floa
   // one lane per 8 columns where the row fits the workgroup
   int lanes = (H / 8 + 63) / 64 * 64;
   if (lanes > 1024) lanes = 1024;
-#define MOE_FIN_BWD(A, B)                                                                     \
-  finalize_backward_kernel<A, B><<<T < kMaxBlocks ? T : kMaxBlocks, lanes, 0, st>>>(     \
+  // All slots together read dout once (T = 8192, k = 8, H = 5120: 399 us; 4 slots
+  // 419, 2 slots 447); few tokens spread their slots over more workgroups.
+  const int tb = T < kMaxBlocks ? T : kMaxBlocks;
+  const bool nt = (long long)T * k * H * (4 + (dy_bf16 ? 2 : 4)) > kStreamBytes;
+#define MOE_FIN_BWD(A, B, SL, NT)                                                            \
+  finalize_backward_kernel<A, B, SL, NT><<<dim3(tb, (k + SL - 1) / SL), lanes, 0, st>>>(      \
       dout, y, pair_pos, w, T, k, H, dy, dw)
+#define MOE_FIN_BWD_BY_SIZE(A, B)            \
+  if (T < 512)                               \
+    MOE_FIN_BWD(A, B, 2, false);             \
+  else if (nt)                               \
+    MOE_FIN_BWD(A, B, 8, true);              \
+  else                                       \
+    MOE_FIN_BWD(A, B, 8, false)
   if (dout_bf16) {
-    if (dy_bf16)
-      MOE_FIN_BWD(true, true);
-    else
-      MOE_FIN_BWD(true, false);
+    if (dy_bf16) {
+      MOE_FIN_BWD_BY_SIZE(true, true);
+    } else {
+      MOE_FIN_BWD_BY_SIZE(true, false);
+    }
   } else {
-    if (dy_bf16)
-      MOE_FIN_BWD(false, true);
-    else
-      MOE_FIN_BWD(false, false);
+    if (dy_bf16) {
+      MOE_FIN_BWD_BY_SIZE(false, true);
+    } else {
+      MOE_FIN_BWD_BY_SIZE(false, false);
+    }
   }
+#undef MOE_FIN_BWD_BY_SIZE
 #undef MOE_FIN_BWD
   return hipGetLastError();
 }

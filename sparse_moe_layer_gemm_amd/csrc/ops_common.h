@@ -23,6 +23,22 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t d) { return __uint_as_float(d << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t d) { return __uint_as_float(d & 0xFFFF0000u); }
 
+// Loads and stores of values that are used once: NT ones leave the caches to
+// others. Elementwise calls take them when they move more than kStreamBytes (the
+// caches hold 256 MB; what a small call writes, the next one finds there).
+constexpr long long kStreamBytes = 128ll << 20;
+template <bool NT, class T>
+__device__ __forceinline__ T load_once(const T* p) {
+  return NT ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool NT, class T>
+__device__ __forceinline__ void store_once(T* p, const T& v) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+
 // Rows [lo, lo + cnt) of expert e, with bounds outside [0, M] taken as 0 or M.
 __device__ __forceinline__ void expert_rows(const int32_t* __restrict__ offsets, int e, int M,
                                             int& lo, int& cnt) {
