@@ -37,10 +37,6 @@ int64_t span(int64_t rows, int64_t row_bytes) {
   return rows * row_bytes;
 }
 
-// Whether the experts average few enough rows that their weights, not the
-// matrix instructions, bound a product.
-bool few_rows(int64_t M, int32_t E) { return M <= 32 * (int64_t)E; }
-
 int32_t scale_stride(int32_t K) { return (K / 32 + 3) / 4 * 4; }
 
 moe_status check_grouped(int64_t a_rows, const int32_t* row_index, int32_t row_div, int64_t M,
@@ -84,8 +80,9 @@ moe_status moe_grouped_gemm(const void* a, int32_t dtype, int64_t a_rows, const 
   const moe::GroupedLayout lay = w_trans ? moe::G_NT : moe::G_NN;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (dtype == MOE_F32) return launch_status(moe::launch_grouped_simple(moe::G_F32, lay, g, st));
-  return launch_status(few_rows(M, E) ? moe::launch_grouped_stream(moe::G_BF16, lay, g, st)
-                                      : moe::launch_grouped_tile(lay, g, st));
+  return launch_status(moe::prefer_stream(moe::G_BF16, g)
+                           ? moe::launch_grouped_stream(moe::G_BF16, lay, g, st)
+                           : moe::launch_grouped_tile(lay, g, st));
 }
 
 moe_status moe_grouped_wgrad(const void* a, int32_t dtype, int64_t a_rows, const int32_t* row_index,
@@ -233,8 +230,9 @@ moe_status moe_mxfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scale
   moe::GroupedArgs g{a_codes, a_scales, a_rows, row_index, row_div, w_codes, w_scales, (int)M, K, N,
                      E, S, offsets, out, out_dtype == MOE_BF16, false};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  return launch_status(few_rows(M, E) ? moe::launch_grouped_stream(moe::G_MX, moe::G_NT, g, st)
-                                      : moe::launch_mxfp4_tile(g, st));
+  return launch_status(moe::prefer_stream(moe::G_MX, g)
+                           ? moe::launch_grouped_stream(moe::G_MX, moe::G_NT, g, st)
+                           : moe::launch_mxfp4_tile(g, st));
 }
 
 }  // extern "C"

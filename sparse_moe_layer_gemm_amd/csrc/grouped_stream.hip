@@ -1,15 +1,18 @@
 // Grouped products for experts with few rows (decode): out[r] = a[i(r)] . w[e]
 // for bf16 weights stored [K, N] or [N, K] and for MXFP4 rows and weights.
 //
-// Bound by the weight stream, so the shape is chosen for loads in flight: a
-// workgroup takes 64 columns of one expert and up to 16 RT of its rows, its
-// four wavefronts a quarter of the depth each. Every wavefront streams through
-// a private ring of LDS stages filled by direct global -> LDS loads, without a
-// barrier until the end, where the four partial sums are added in order. The
-// rows (a few KB, in L2) come through the same ring. Fragments, swizzles and
-// zeros outside the operands as in grouped_tile.hip; the MFMA is 16x16x32
-// bf16, or the block-scaled 16x16x128 for MXFP4 (lane l: row l % 16, block
-// l / 16 of the step's four).
+// Bound by the weight stream, so the shape is chosen for lines in flight: a
+// workgroup takes 64 columns of one expert and up to 16 RT of its rows, its WV
+// wavefronts a part of the depth each. Every wavefront streams through a
+// private ring of D LDS stages filled by direct global -> LDS loads of whole
+// 128-byte lines, without a barrier until the end, where the partial sums are
+// added in order. The rows (a few KB, in L2) come through the same ring. A CU
+// tracks about 500 loads in flight, whatever their size, so 64-byte pieces and
+// loads of single scales halve the rate: the scales of the 64 columns, one
+// contiguous block over the whole depth, are copied to LDS at the start.
+// Fragments, swizzles and zeros outside the operands as in grouped_tile.hip; the
+// MFMA is 16x16x32 bf16, or the block-scaled 16x16x128 for MXFP4 (lane l: row
+// l % 16, block l / 16 of four).
 #include "grouped_common.h"
 
 namespace moe {
@@ -18,21 +21,36 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 enum { S_NN = 0, S_NT = 1, S_MX = 2 };
-constexpr int WAVES = 4, BN = 64;
+constexpr int BN = 64;
 
-__device__ __forceinline__ int swz_row(int row) { return (row >> 2) & 2; }
-// granule g (of 8) of depth row k (128 bytes) sits at g ^ 2 f(k)
+// granule g (of 8) of a 128-byte row sits at g ^ swz_row(row), of depth row k
+// (128 bytes of 64 columns) at g ^ swz_depth(k); of a 64-byte row at g ^ swz_half(row)
+__device__ __forceinline__ int swz_row(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int swz_half(int row) { return (row >> 2) & 2; }
 __device__ __forceinline__ int swz_depth(int k) { return (k & 2) | ((k >> 1) & 4); }
 
-// Reads of one step and the wait that publishes them.
+template <int KIND, int RT, int WV, int D>
+struct StreamShape {
+  static constexpr bool ROWS = KIND != S_NN;         // w contiguous along the depth
+  static constexpr int SUB = ROWS ? 2 : 1;           // MFMA depths per step
+  static constexpr int WB = ROWS ? 8192 : 4096;      // LDS bytes of w's and a's part of a stage
+  static constexpr int AB = (ROWS ? 2048 : 1024) * RT;
+  static constexpr int STAGE = WB + AB, RING = D * STAGE;
+  static constexpr int WL = WB / 1024, AL = AB / 1024, LOADS = WL + AL;
+  static constexpr int DEPTH = KIND == S_NN ? 32 : KIND == S_NT ? 64 : 256;  // of a step
+  static constexpr int RINGS = WV * RING;
+  static_assert(WV * RT * 4096 <= RINGS, "partial sums reuse the rings");
+};
+
+// Reads of one MFMA depth and the wait that publishes them.
 template <int KIND, int RT>
-struct Step {
+struct Sub {
   u32x4 a[RT], w[4];
   u32x2 lo[4], hi[4];
   uint32_t sa[RT], sw[4];
 };
 template <int KIND, int RT>
-__device__ __forceinline__ void wait_step(Step<KIND, RT>& f) {
+__device__ __forceinline__ void wait_sub(Sub<KIND, RT>& f) {
 #pragma unroll
   for (int i = 0; i < RT; ++i) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(f.a[i])::"memory");
 #pragma unroll
@@ -49,84 +67,92 @@ __device__ __forceinline__ void wait_step(Step<KIND, RT>& f) {
     for (int j = 0; j < 4; ++j) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(f.sw[j])::"memory");
   }
 }
+__device__ __forceinline__ uint32_t lds_byte(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ds_read_u8 %0, %1" : "=v"(r) : "v"(addr));
+  return r;
+}
 
-template <int KIND, int RT, int D>
-struct StreamShape {
-  static constexpr int SCALES = KIND == S_MX ? 512 : 0;  // 64 row dwords of w, then of a
-  static constexpr int STAGE = 4096 + 1024 * RT + SCALES;
-  static constexpr int RING = D * STAGE;
-  static constexpr int LOADS = 4 + RT + (KIND == S_MX ? 2 : 0);
-  static constexpr int LDS = WAVES * RING;
-  static_assert(WAVES * RT * 4096 <= LDS, "partial sums reuse the rings");
-};
-
-template <int KIND, int RT, int D>
-__global__ __launch_bounds__(64 * WAVES, 2) void grouped_stream_kernel(GroupedArgs g, int nt) {
-  using S = StreamShape<KIND, RT, D>;
-  __shared__ __align__(1024) uint8_t smem[S::LDS];
+// Dynamic LDS (MXFP4): the scales of the 64 columns, then of the rows, S bytes each.
+template <int KIND, int RT, int WV, int D>
+__global__ __launch_bounds__(64 * WV, 2) void grouped_stream_kernel(GroupedArgs g, int nt) {
+  using S = StreamShape<KIND, RT, WV, D>;
+  __shared__ __align__(1024) uint8_t smem[S::RINGS];
+  extern __shared__ __align__(1024) uint8_t scales[];
   RowTile t;
   if (!find_tile<16 * RT, 8>(g, nt, t)) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int n0 = BN * t.nt;
-  constexpr int KS = KIND == S_MX ? 128 : 32;              // depth of a step: 64 bytes of a row
-  const int rb = KIND == S_MX ? g.K / 2 : 2 * g.K;         // bytes per row
-  const int nk = (g.K + KS - 1) / KS, per = (nk + WAVES - 1) / WAVES;
-  const int kb = wave * per, ke = min(nk, kb + per);       // this wavefront's steps
+  const int rb = KIND == S_MX ? g.K / 2 : 2 * g.K;  // bytes per row
+  const int nk = (g.K + S::DEPTH - 1) / S::DEPTH, per = (nk + WV - 1) / WV;
+  const int kb = wave * per, ke = min(nk, kb + per);  // this wavefront's steps
   const char* const zeros = reinterpret_cast<const char*>(kZeros);
-  const char* A = static_cast<const char*>(g.a);
-  const char* W = static_cast<const char*>(g.w);
+  const char* const A = static_cast<const char*>(g.a);
+  const char* const W = static_cast<const char*>(g.w);
   uint8_t* ring = smem + wave * S::RING;
 
   // ---- direct loads of a step (1 KB each); lim: steps with the lane's part inside
-  const char *ap[RT], *wp[4], *sap = zeros, *swp = zeros;
-  int alim[RT], wlim[4], salim = 0, swlim = 0;
+  const char *ap[S::AL], *wp[S::WL];
+  int alim[S::AL], wlim[S::WL];
 #pragma unroll
-  for (int q = 0; q < RT; ++q) {
-    const int row = 16 * q + (lane >> 2), lg = (lane & 3) ^ swz_row(row);
+  for (int q = 0; q < S::AL; ++q) {
+    const int row = S::ROWS ? 8 * q + (lane >> 3) : 16 * q + (lane >> 2);
+    const int lg = S::ROWS ? (lane & 7) ^ swz_row(row) : (lane & 3) ^ swz_half(row);
     const int s = t.m0 + row < t.cnt ? source_row(g, t.lo + t.m0 + row) : -1;
+    constexpr int SB = S::ROWS ? 128 : 64;  // bytes of a row per step
     ap[q] = A + (size_t)(s < 0 ? 0 : s) * rb + 16 * lg;
-    alim[q] = s < 0 ? 0 : min(ke, (rb - 16 * lg + 63) >> 6);
+    alim[q] = s < 0 ? 0 : min(ke, (rb - 16 * lg + SB - 1) / SB);
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if constexpr (KIND == S_NN) {
+  for (int q = 0; q < S::WL; ++q) {
+    if constexpr (!S::ROWS) {
       const int k = 8 * q + (lane >> 3), c = n0 + 8 * ((lane & 7) ^ swz_depth(k));
       wp[q] = W + (((size_t)t.e * g.K + k) * g.N + (c < g.N ? c : 0)) * 2;
       wlim[q] = min(ke, (g.K - k + 31) >> 5);
     } else {
-      const int row = 16 * q + (lane >> 2), lg = (lane & 3) ^ swz_row(row);
+      const int row = 8 * q + (lane >> 3), lg = (lane & 7) ^ swz_row(row);
       const bool ok = n0 + row < g.N;
       wp[q] = W + ((size_t)t.e * g.N + (ok ? n0 + row : 0)) * rb + 16 * lg;
-      wlim[q] = ok ? min(ke, (rb - 16 * lg + 63) >> 6) : 0;
+      wlim[q] = ok ? min(ke, (rb - 16 * lg + 127) >> 7) : 0;
     }
   }
-  if constexpr (KIND == S_MX) {
-    const bool ok = n0 + lane < g.N;
-    swp = reinterpret_cast<const char*>(g.w_scale) + ((size_t)t.e * g.N + (ok ? n0 + lane : 0)) * g.S;
-    swlim = ok ? ke : 0;
-    const int s = (lane < 16 * RT && t.m0 + lane < t.cnt) ? source_row(g, t.lo + t.m0 + lane) : -1;
-    sap = reinterpret_cast<const char*>(g.a_scale) + (size_t)(s < 0 ? 0 : s) * g.S;
-    salim = s < 0 ? 0 : ke;
-  }
-  const size_t wstep = KIND == S_NN ? (size_t)g.N * 64 : 64;
+  const size_t wstep = KIND == S_NN ? (size_t)g.N * 64 : 128;
   auto issue = [&](int kt, int st) {
     uint8_t* p = ring + st * S::STAGE;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) dma16(kt < wlim[q] ? wp[q] + kt * wstep : zeros, p + 1024 * q);
+    for (int q = 0; q < S::WL; ++q) dma16(kt < wlim[q] ? wp[q] + kt * wstep : zeros, p + 1024 * q);
 #pragma unroll
-    for (int q = 0; q < RT; ++q)
-      dma16(kt < alim[q] ? ap[q] + (size_t)kt * 64 : zeros, p + 4096 + 1024 * q);
-    if constexpr (KIND == S_MX) {
-      dma4(kt < swlim ? swp + 4 * kt : zeros, p + 4096 + 1024 * RT);
-      dma4(kt < salim ? sap + 4 * kt : zeros, p + 4096 + 1024 * RT + 256);
-    }
+    for (int q = 0; q < S::AL; ++q)
+      dma16(kt < alim[q] ? ap[q] + (size_t)kt * (S::ROWS ? 128 : 64) : zeros, p + S::WB + 1024 * q);
   };
+  const int sa0 = (BN * g.S + 1023) & ~1023;  // where the rows' scales start
+  if constexpr (KIND == S_MX) {
+    const char* ws = reinterpret_cast<const char*>(g.w_scale) + ((size_t)t.e * g.N + n0) * g.S;
+    const int have = min(BN, g.N - n0) * g.S;
+    for (int o = 1024 * wave; o < BN * g.S; o += 1024 * WV)
+      dma16(o + 16 * lane < have ? ws + o + 16 * lane : zeros, scales + o);
+    const int s4 = g.S >> 2;
+    for (int o = 64 * wave; o < 16 * RT * s4; o += 64 * WV) {
+      const int i = o + lane, row = i / s4, d = i - row * s4;
+      const int s = (row < 16 * RT && t.m0 + row < t.cnt) ? source_row(g, t.lo + t.m0 + row) : -1;
+      dma4(s >= 0 ? reinterpret_cast<const char*>(g.a_scale) + (size_t)s * g.S + 4 * d : zeros,
+           scales + sa0 + 4 * o);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < D; ++s) issue(kb + s, s);
+  if constexpr (KIND == S_MX) {  // everyone's scales
+    wait_loads<D * S::LOADS>();
+    __builtin_amdgcn_s_barrier();
+  }
 
   // ---- fragment addresses
   const int l16 = lane & 15, kg = lane >> 4;
-  const uint32_t lds0 = (uint32_t)(size_t)(lds_u8*)ring;
-  const uint32_t rowaddr = lds0 + l16 * 64 + ((kg ^ swz_row(l16)) << 4);
-  uint32_t coladdr[4];
+  const uint32_t lds0 = (uint32_t)(size_t)(lds_u8*)ring, lds_s = (uint32_t)(size_t)(lds_u8*)scales;
+  uint32_t rowaddr[2], coladdr[4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) rowaddr[m] = lds0 + l16 * 128 + (((4 * m + kg) ^ swz_row(l16)) << 4);
+  const uint32_t halfaddr = lds0 + S::WB + l16 * 64 + ((kg ^ swz_half(l16)) << 4);
   const int kr = 8 * kg + (l16 >> 2);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -139,39 +165,36 @@ __global__ __launch_bounds__(64 * WAVES, 2) void grouped_stream_kernel(GroupedAr
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-#pragma unroll
-  for (int s = 0; s < D; ++s) issue(kb + s, s);
-  int st = 0;
-  for (int kt = kb; kt < ke; ++kt) {
-    wait_loads<(D - 1) * S::LOADS>();
-    Step<KIND, RT> f;
-    const uint32_t off = st * S::STAGE;
+  auto read_sub = [&](Sub<KIND, RT>& f, uint32_t off, int kt, auto mm) {
+    constexpr int m = decltype(mm)::value;
     static_for<4>([&](auto jj) {
       constexpr int j = decltype(jj)::value;
       if constexpr (KIND == S_NN) {
         f.lo[j] = lds_tr16<0>(coladdr[j] + off);
         f.hi[j] = lds_tr16<512>(coladdr[j] + off);
       } else {
-        f.w[j] = lds_b128<1024 * j>(rowaddr + off);
+        f.w[j] = lds_b128<2048 * j>(rowaddr[m] + off);
       }
-      if constexpr (KIND == S_MX) f.sw[j] = lds_b32<4096 + 1024 * RT + 64 * j>(lds0 + 4 * l16 + off);
+      if constexpr (KIND == S_MX)
+        f.sw[j] = lds_byte(lds_s + (16 * j + l16) * g.S + 8 * kt + 4 * m + kg);
     });
     static_for<RT>([&](auto ii) {
       constexpr int i = decltype(ii)::value;
-      f.a[i] = lds_b128<4096 + 1024 * i>(rowaddr + off);
+      if constexpr (KIND == S_NN)
+        f.a[i] = lds_b128<1024 * i>(halfaddr + off);
+      else
+        f.a[i] = lds_b128<S::WB + 2048 * i>(rowaddr[m] + off);
       if constexpr (KIND == S_MX)
-        f.sa[i] = lds_b32<4096 + 1024 * RT + 256 + 64 * i>(lds0 + 4 * l16 + off);
+        f.sa[i] = lds_byte(lds_s + sa0 + (16 * i + l16) * g.S + 8 * kt + 4 * m + kg);
     });
-    wait_step(f);
-    issue(kt + D, st);
-    st = st + 1 == D ? 0 : st + 1;
+  };
+  auto mfma_sub = [&](Sub<KIND, RT>& f, int kt, int m) {
     if constexpr (KIND == S_MX) {
-      // block kg of the step; bytes past K / 32 count as zero
-      const uint32_t width = 4 * kt + kg < g.K / 32 ? 8u : 0u;
+      const uint32_t keep = 8 * kt + 4 * m + kg < g.K / 32 ? 255u : 0u;  // no scales past K / 32
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f.sw[j] = __builtin_amdgcn_ubfe(f.sw[j], 8 * kg, width);
+      for (int j = 0; j < 4; ++j) f.sw[j] &= keep;
 #pragma unroll
-      for (int i = 0; i < RT; ++i) f.sa[i] = __builtin_amdgcn_ubfe(f.sa[i], 8 * kg, width);
+      for (int i = 0; i < RT; ++i) f.sa[i] &= keep;
     }
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -193,8 +216,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void grouped_stream_kernel(GroupedAr
                                                               acc[i][j], 0, 0, 0);
         }
       }
+  };
+  int st = 0;
+  for (int kt = kb; kt < ke; ++kt) {
+    wait_loads<(D - 1) * S::LOADS>();
+    Sub<KIND, RT> f[S::SUB];
+    const uint32_t off = st * S::STAGE;
+    static_for<S::SUB>([&](auto mm) { read_sub(f[decltype(mm)::value], off, kt, mm); });
+    static_for<S::SUB>([&](auto mm) { wait_sub(f[decltype(mm)::value]); });
+    issue(kt + D, st);
+    st = st + 1 == D ? 0 : st + 1;
+    static_for<S::SUB>([&](auto mm) { mfma_sub(f[decltype(mm)::value], kt, decltype(mm)::value); });
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  wait_loads<0>();
   __syncthreads();
 
   // ---- partial sums: wavefront w's at w * RT * 4 KB, rows of 64 fp32 (granule c of
@@ -207,13 +241,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void grouped_stream_kernel(GroupedAr
       *reinterpret_cast<f32x4*>(part + ((wave * RT + i) * 16 + l16) * 64 + (((4 * j + kg) ^ l16) << 2)) =
           acc[i][j];
   __syncthreads();
-  const int r = tid >> 4, c = tid & 15, n = n0 + 4 * c;
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int m = t.m0 + 16 * i + r;
+  for (int id = tid; id < 256 * RT; id += 64 * WV) {
+    const int i = id >> 8, r = (id >> 4) & 15, c = id & 15, n = n0 + 4 * c, m = t.m0 + 16 * i + r;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
+    for (int w = 0; w < WV; ++w) {
       const f32x4 p = *reinterpret_cast<const f32x4*>(part + ((w * RT + i) * 16 + r) * 64 + ((c ^ r) << 2));
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] += p[q];
@@ -229,23 +261,50 @@ __global__ __launch_bounds__(64 * WAVES, 2) void grouped_stream_kernel(GroupedAr
   }
 }
 
-template <int KIND, int RT, int D>
-hipError_t launch(const GroupedArgs& a, hipStream_t st) {
-  const int nt = (a.N + BN - 1) / BN;
-  const long long n = (max_row_tiles(a.M, a.E, 16 * RT) * nt + 7) / 8 * 8;
-  if (n * 64 * WAVES >= (1LL << 32)) return hipErrorInvalidValue;
-  grouped_stream_kernel<KIND, RT, D><<<(unsigned)n, 64 * WAVES, 0, st>>>(a, nt);
-  return hipGetLastError();
+// Whole 1 KB loads of w's scales, whole 256-byte loads of a's, and what a step past
+// the last row's scales reads.
+constexpr int scale_bytes(int S, int RT) {
+  return ((BN * S + 1023) & ~1023) + ((16 * RT * S + 255) & ~255) + 16;
 }
 
+template <int KIND, int RT, int WV, int D>
+hipError_t launch(const GroupedArgs& a, hipStream_t st) {
+  using S = StreamShape<KIND, RT, WV, D>;
+  const int nt = (a.N + BN - 1) / BN;
+  const long long n = (max_row_tiles(a.M, a.E, 16 * RT) * nt + 7) / 8 * 8;
+  if (n * 64 * WV >= (1LL << 32)) return hipErrorInvalidValue;
+  const int scales = KIND == S_MX ? scale_bytes(a.S, RT) : 0;
+  grouped_stream_kernel<KIND, RT, WV, D><<<(unsigned)n, 64 * WV, scales, st>>>(a, nt);
+  return hipGetLastError();
+}
 }  // namespace
+
+// The streaming kernel or the 256 x 256 tiles? Measured at K = 5120, N = 1536, us
+// (bf16 w [K, N] / MXFP4), streaming against tiles:
+//   64 experts (384 tiles), rows per expert 4: 177 / 50 against 178 / 70; 8: 188 / 59
+//     against 182 / 71; 16: 211 / 70 against 187 / 72; 32: 240 / 108 against 197 / 75
+//   24 experts (144 tiles), 8: 83 / 23 against 76 / 24; 32: 106 / 41 against 100 / 32
+//   8 experts (48 tiles), 16: 35 / 12 against 49 / 21; 64: 38 / 22 against 87 / 31
+//   1 expert (6 tiles), 64: 20 / 11 against 49 / 16
+// So: few rows per expert, where the weights bound both; or so few tiles that
+// they leave half of the 256 CUs idle, while the streaming workgroups (four to
+// a tile's columns, up to 32 rows each) still run side by side, two per CU. The
+// scales of MXFP4 columns have to fit in LDS.
+bool prefer_stream(GroupedInput in, const GroupedArgs& a) {
+  if (in == G_MX && scale_bytes(a.S, 2) > 40 * 1024) return false;
+  const long long e = a.E < a.M ? a.E : a.M;
+  if (a.M <= (in == G_MX ? 16 : 8) * e) return true;
+  const long long tiles = e * ((a.N + 255) / 256), streams = e * ((a.N + BN - 1) / BN) * ((a.M + 32 * e - 1) / (32 * e));
+  return tiles < 128 && streams <= 512;
+}
 
 hipError_t launch_grouped_stream(GroupedInput in, GroupedLayout lay, const GroupedArgs& a,
                                  hipStream_t st) {
   const bool wide = a.M > 16LL * a.E;  // more than 16 rows per expert on average
-  if (in == G_MX) return wide ? launch<S_MX, 2, 3>(a, st) : launch<S_MX, 1, 3>(a, st);
-  if (lay == G_NN) return wide ? launch<S_NN, 2, 3>(a, st) : launch<S_NN, 1, 4>(a, st);
-  return wide ? launch<S_NT, 2, 3>(a, st) : launch<S_NT, 1, 4>(a, st);
+  // wavefronts and stages so that two workgroups (MXFP4: three) share a CU's LDS
+  if (in == G_MX) return wide ? launch<S_MX, 2, 3, 2>(a, st) : launch<S_MX, 1, 3, 2>(a, st);
+  if (lay == G_NN) return wide ? launch<S_NN, 2, 4, 3>(a, st) : launch<S_NN, 1, 4, 4>(a, st);
+  return wide ? launch<S_NT, 2, 3, 2>(a, st) : launch<S_NT, 1, 4, 2>(a, st);
 }
 
 }  // namespace moe

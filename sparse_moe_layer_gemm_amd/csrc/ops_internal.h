@@ -40,6 +40,7 @@ hipError_t launch_grouped_tile(GroupedLayout lay, const GroupedArgs& a, hipStrea
 // bf16 and MXFP4 products of experts with few rows: the weights are streamed.
 hipError_t launch_grouped_stream(GroupedInput in, GroupedLayout lay, const GroupedArgs& a,
                                  hipStream_t st);
+bool prefer_stream(GroupedInput in, const GroupedArgs& a);
 // MXFP4 products on 256 x 256 tiles of the block-scaled fp4 MFMA.
 hipError_t launch_mxfp4_tile(const GroupedArgs& a, hipStream_t st);
 

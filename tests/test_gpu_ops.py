@@ -58,6 +58,14 @@ SHAPES = [
     ([1] * 9, 1544, 200),
     ([2, 1, 4] * 21, 320, 512),
     ([700], 1032, 776),
+    # many tiles or long experts: the tiled kernels
+    ([2000, 0, 1, 700, 255, 2500], 544, 328),
+    ([4000], 1032, 776),
+    ([65, 129, 257] * 22, 200, 520),
+    ([0, 40, 96, 3, 200, 33, 64] * 10, 136, 520),
+    ([300, 31, 600], 64, 16392),
+    # one long expert among short ones: the streaming kernels
+    ([300] + [0, 1] * 40, 320, 200),
 ]
 
 
@@ -143,7 +151,7 @@ def test_grouped_no_rows():
 
 
 @pytest.mark.parametrize("layout", ["nn", "nt", "mx"])
-@pytest.mark.parametrize("per", [2, 300])
+@pytest.mark.parametrize("per", [2, 300, 3000])
 def test_bad_rows_stay_where_they_are(layout, per):
     """An infinity or a NaN in one row reaches that row's products only; bounds outside [0, M] are clamped."""
     g, E, K, N = gen(3), 3, 256, 264
