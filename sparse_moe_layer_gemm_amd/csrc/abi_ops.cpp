@@ -16,6 +16,7 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSorted = int64_t(1) << 29;  // rows of a grouped product (grid size)
 constexpr int32_t kMaxWidth = 1 << 20;            // K and N of a grouped product
 constexpr int64_t kMaxBytes = int64_t(1) << 46;  // no array is larger than the address space
+constexpr int64_t kMaxScales = 0xFFF00000ll;       // bytes of a's MXFP4 scales (32-bit buffer offsets)
 constexpr int64_t kMaxLanes = (int64_t(1) << 32) - 1;  // lanes of one grid dimension
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 
@@ -43,7 +44,7 @@ moe_status check_grouped(int64_t a_rows, const int32_t* row_index, int32_t row_d
                          int32_t K, int32_t N, int32_t E, int32_t k_unit) {
   if (M < 0 || K <= 0 || N <= 0 || E <= 0 || a_rows < 0) return MOE_ERR_INVALID_ARGUMENT;
   if (E > 256 || K % k_unit != 0 || N % 8 != 0 || K > kMaxWidth || N > kMaxWidth ||
-      M >= kMaxSorted || a_rows > kMaxRows)
+      M >= kMaxSorted || a_rows > kMaxRows || !moe::grouped_fits(M, K, N, E))
     return MOE_ERR_UNSUPPORTED;
   if (row_index) {
     if (row_div < 1) return MOE_ERR_INVALID_ARGUMENT;
@@ -79,7 +80,7 @@ moe_status moe_grouped_gemm(const void* a, int32_t dtype, int64_t a_rows, const 
                      offsets, out, out_dtype == MOE_BF16, false};
   const moe::GroupedLayout lay = w_trans ? moe::G_NT : moe::G_NN;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (dtype == MOE_F32) return launch_status(moe::launch_grouped_simple(moe::G_F32, lay, g, st));
+  if (dtype == MOE_F32) return launch_status(moe::launch_grouped_simple(lay, g, st));
   return launch_status(moe::prefer_stream(moe::G_BF16, g)
                            ? moe::launch_grouped_stream(moe::G_BF16, lay, g, st)
                            : moe::launch_grouped_tile(lay, g, st));
@@ -106,7 +107,7 @@ moe_status moe_grouped_wgrad(const void* a, int32_t dtype, int64_t a_rows, const
                      offsets, dw, out_dtype == MOE_BF16, accumulate == 1};
   hipStream_t st = static_cast<hipStream_t>(stream);
   return launch_status(dtype == MOE_BF16 ? moe::launch_grouped_tile(moe::G_TN, g, st)
-                                         : moe::launch_grouped_simple(moe::G_F32, moe::G_TN, g, st));
+                                         : moe::launch_grouped_simple(moe::G_TN, g, st));
 }
 
 static moe_status check_swiglu(const void* a, int32_t dtype, int64_t M, int32_t I) {
@@ -220,6 +221,7 @@ moe_status moe_mxfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scale
       !array_ok(offsets) || !array_ok(out) || !aligned16(row_index))
     return MOE_ERR_INVALID_ARGUMENT;
   const int32_t S = scale_stride(K);
+  if (a_rows * S > kMaxScales) return MOE_ERR_UNSUPPORTED;
   const int64_t ab = span(a_rows, K / 2), wb = span((int64_t)E * N, K / 2),
                 ob = span(M, N * elem(out_dtype));
   if (ab < 0 || wb < 0 || ob < 0) return MOE_ERR_UNSUPPORTED;

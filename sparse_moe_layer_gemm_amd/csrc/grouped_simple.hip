@@ -1,12 +1,11 @@
-// Grouped products in fp32 for any input type: out[r] = a[i(r)] . w[e] for the
-// rows r of each expert, and the weight gradient dw[e] = sum a[i(r)]^T . d[r].
+// Grouped products of the fp32 layer: out[r] = a[i(r)] . w[e] for the rows r of
+// each expert, and the weight gradient dw[e] = sum a[i(r)]^T . d[r].
 //
 // A workgroup computes one 64 x 64 tile of one expert: 16-deep slices of both
-// operands go through LDS as fp32 (bf16 and MXFP4 values are exact there) and
-// four wavefronts of 32 x 32 feed the fp32 MFMA 32x32x2. Every load checks its
-// row, column and depth, so any size works. Bound: fp32 MFMA and the scalar
-// loads in front of it; this is the path of the fp32 layer, where exactness
-// counts, not the one that large products take.
+// operands go through LDS and four wavefronts of 32 x 32 feed the fp32 MFMA
+// 32x32x2. Every load checks its row, column and depth, so any size works.
+// Bound: the scalar loads and the barriers around each slice (0.07 PFLOP/s);
+// this path is for exactness, not for large products.
 #include "ops_common.h"
 
 namespace moe {
@@ -33,26 +32,10 @@ __device__ __forceinline__ bool find_rows(const GroupedArgs& g, int item, int& e
   return false;
 }
 
-template <int IN>
-__device__ __forceinline__ float load_elem(const void* base, const uint8_t* scale, long long row,
-                                           int ld, int S, int c) {
-  if constexpr (IN == G_BF16)
-    return bf16_bits_to_f32(static_cast<const uint16_t*>(base)[row * ld + c]);
-  else if constexpr (IN == G_F32)
-    return static_cast<const float*>(base)[row * ld + c];
-  else {
-    const uint32_t byte = static_cast<const uint8_t*>(base)[row * (ld / 2) + c / 2];
-    const uint32_t q = (c & 1) ? byte >> 4 : byte & 15u;
-    const uint32_t b = scale[row * S + c / 32];
-    if (b == 255u) return __uint_as_float(0x7FC00000u);
-    const uint32_t ex = (q >> 1) & 3u, man = q & 1u;
-    const float mag = ex ? (float)((2u + man) << (ex - 1)) * 0.5f : 0.5f * (float)man;
-    return __builtin_ldexpf((q & 8u) ? -mag : mag, (int)b - 127);
-  }
-}
-
-template <int IN, int LAY>
+template <int LAY>
 __global__ __launch_bounds__(256) void grouped_simple_kernel(GroupedArgs g) {
+  const float* const A = static_cast<const float*>(g.a);
+  const float* const W = static_cast<const float*>(g.w);
   __shared__ float As[BK][LDP], Bs[BK][LDP];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int wm = wave >> 1, wn = wave & 1, l32 = lane & 31, kh = lane >> 5;
@@ -89,23 +72,22 @@ __global__ __launch_bounds__(256) void grouped_simple_kernel(GroupedArgs g) {
         float va = 0.f, vb = 0.f;
         if (k0 + k < depth) {
           const int r = lo + k0 + k, s = source_row(g, r);
-          if (s >= 0 && m0 + m < g.K) va = load_elem<IN>(g.a, nullptr, s, g.K, 0, m0 + m);
-          if (n0 + m < g.N) vb = load_elem<IN>(g.w, nullptr, r, g.N, 0, n0 + m);
+          if (s >= 0 && m0 + m < g.K) va = A[(size_t)s * g.K + m0 + m];
+          if (n0 + m < g.N) vb = W[(size_t)r * g.N + n0 + m];
         }
         As[k][m] = va;
         Bs[k][m] = vb;
       } else {
         const int k = tid & 15, m = (tid >> 4) + 16 * i;
-        As[k][m] = (arow[i] >= 0 && k0 + k < g.K)
-                       ? load_elem<IN>(g.a, g.a_scale, arow[i], g.K, g.S, k0 + k) : 0.f;
+        As[k][m] = (arow[i] >= 0 && k0 + k < g.K) ? A[(size_t)arow[i] * g.K + k0 + k] : 0.f;
         if constexpr (LAY == G_NT) {
           Bs[k][m] = (n0 + m < g.N && k0 + k < g.K)
-                         ? load_elem<IN>(g.w, g.w_scale, (long long)e * g.N + n0 + m, g.K, g.S, k0 + k)
+                         ? W[((size_t)e * g.N + n0 + m) * g.K + k0 + k]
                          : 0.f;
         } else {
           const int n = tid & 63, kk = (tid >> 6) + 4 * i;
           Bs[kk][n] = (n0 + n < g.N && k0 + kk < g.K)
-                          ? load_elem<IN>(g.w, nullptr, (long long)e * g.K + k0 + kk, g.N, 0, n0 + n)
+                          ? W[((size_t)e * g.K + k0 + kk) * g.N + n0 + n]
                           : 0.f;
         }
       }
@@ -133,26 +115,20 @@ __global__ __launch_bounds__(256) void grouped_simple_kernel(GroupedArgs g) {
   }
 }
 
-template <int IN, int LAY>
+template <int LAY>
 hipError_t launch(const GroupedArgs& g, hipStream_t st) {
   const long long tiles = LAY == G_TN ? (long long)g.E * ((g.K + BT - 1) / BT)
                                       : g.M / BT + (long long)(g.E < g.M ? g.E : g.M);
   if (tiles > 0x7fffffffLL) return hipErrorInvalidValue;
   const dim3 grid((unsigned)tiles, (unsigned)((g.N + BT - 1) / BT));
-  grouped_simple_kernel<IN, LAY><<<grid, 256, 0, st>>>(g);
+  grouped_simple_kernel<LAY><<<grid, 256, 0, st>>>(g);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_grouped_simple(GroupedInput in, GroupedLayout lay, const GroupedArgs& a,
-                                 hipStream_t st) {
-  if (in == G_MX) return lay == G_NT ? launch<G_MX, G_NT>(a, st) : hipErrorInvalidValue;
-  if (in == G_F32)
-    return lay == G_NN ? launch<G_F32, G_NN>(a, st)
-                       : lay == G_NT ? launch<G_F32, G_NT>(a, st) : launch<G_F32, G_TN>(a, st);
-  return lay == G_NN ? launch<G_BF16, G_NN>(a, st)
-                     : lay == G_NT ? launch<G_BF16, G_NT>(a, st) : launch<G_BF16, G_TN>(a, st);
+hipError_t launch_grouped_simple(GroupedLayout lay, const GroupedArgs& a, hipStream_t st) {
+  return lay == G_NN ? launch<G_NN>(a, st) : lay == G_NT ? launch<G_NT>(a, st) : launch<G_TN>(a, st);
 }
 
 }  // namespace moe

@@ -271,7 +271,7 @@ template <int KIND, int RT, int WV, int D>
 hipError_t launch(const GroupedArgs& a, hipStream_t st) {
   using S = StreamShape<KIND, RT, WV, D>;
   const int nt = (a.N + BN - 1) / BN;
-  const long long n = (max_row_tiles(a.M, a.E, 16 * RT) * nt + 7) / 8 * 8;
+  const long long n = tile_grid(a, 16 * RT, nt);
   if (n * 64 * WV >= (1LL << 32)) return hipErrorInvalidValue;
   const int scales = KIND == S_MX ? scale_bytes(a.S, RT) : 0;
   grouped_stream_kernel<KIND, RT, WV, D><<<(unsigned)n, 64 * WV, scales, st>>>(a, nt);

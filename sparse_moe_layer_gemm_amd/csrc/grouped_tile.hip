@@ -4,8 +4,8 @@
 //
 // One workgroup of 8 wavefronts (2 x 4) computes a 256 x 256 tile of one
 // expert, 128 x 64 per wavefront (8 x 4 MFMA 16x16x32 tiles, 128 accumulators);
-// an expert's last tile of at most 128 (64) rows keeps 64 (32) rows per
-// wavefront, so that short experts pay for their weights, not for padding.
+// an expert's last tile of at most 192, 128 or 64 rows keeps 96, 64 or 32 rows
+// per wavefront, so that short experts pay for their weights, not for padding.
 // The depth advances 64 at a time (a pair of 32-deep steps); LDS holds five
 // such pairs of the operands, filled by direct global -> LDS loads. An operand
 // whose rows are contiguous along the depth comes in as 128-byte rows and is
@@ -363,12 +363,14 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, uint8_t* smem, i
   }
 }
 
-// The row tile by the rows that are left: 256, 128 or 64.
+// The row tile by the rows that are left: 256, 192, 128 or 64.
 template <int LAY>
 __device__ __forceinline__ void tile_by_rows(const GroupedArgs& g, uint8_t* smem, int e, int lo,
                                              int cnt, int m0, int n0, int left) {
-  if (left > 128)
+  if (left > 192)
     tile_body<LAY, 8>(g, smem, e, lo, cnt, m0, n0);
+  else if (left > 128)
+    tile_body<LAY, 6>(g, smem, e, lo, cnt, m0, n0);
   else if (left > 64)
     tile_body<LAY, 4>(g, smem, e, lo, cnt, m0, n0);
   else
@@ -407,7 +409,7 @@ hipError_t launch_grouped_tile(GroupedLayout lay, const GroupedArgs& a, hipStrea
     grouped_wgrad_kernel<<<(unsigned)n, lanes, 0, st>>>(a, mt, nt);
     return hipGetLastError();
   }
-  const long long n = (max_row_tiles(a.M, a.E, 256) * nt + 7) / 8 * 8;
+  const long long n = tile_grid(a, 256, nt);
   if (n * lanes >= (1LL << 32)) return hipErrorInvalidValue;
   if (lay == G_NN)
     grouped_tile_kernel<G_NN><<<(unsigned)n, lanes, 0, st>>>(a, nt);

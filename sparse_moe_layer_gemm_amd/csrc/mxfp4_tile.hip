@@ -135,7 +135,7 @@ __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int
     for (int x = 0; x < 2; ++x) at[x] = ag[x] + 128 * d;
 #pragma unroll
     for (int q = 0; q < QA; ++q) {
-      const int o = QA % 2 ? ((wave & 1) ? at[1] : at[0]) : at[q & 1];
+      const int o = QA % 2 && ((wave ^ q) & 1) ? at[1] : QA % 2 ? at[0] : at[q & 1];  // by (wave QA + q) % 2
       uint8_t* p = As + (wave * QA + q) * 1024;
       if constexpr (BIG)
         dma16(arow[q] >= 0 && o < rb ? A + ((size_t)arow[q] * rb + o) : zeros, p);
@@ -152,23 +152,20 @@ __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int
   const int l32 = lane & 31, kh = lane >> 5;
   const uint32_t lds0 = (uint32_t)(size_t)(lds_u8*)smem;
   const int am = wm * 32 * MT, bn = wn * COLS;
-  uint32_t aaddr[4], baddr[4];
-#pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const int gr = ((4 * kh + h) ^ swz_row(l32)) << 4;
-    aaddr[h] = lds0 + (am + l32) * 128 + gr;
-    baddr[h] = lds0 + NST * OPB + (bn + l32) * 128 + gr;
-  }
+  // granule 4 kh + h sits h << 4 away from granule 4 kh, in the XOR sense
+  const int gr0 = ((4 * kh) ^ swz_row(l32)) << 4;
+  const uint32_t aaddr = lds0 + (am + l32) * 128 + gr0, baddr = lds0 + NST * OPB + (bn + l32) * 128 + gr0;
   constexpr int SROW = S16 ? 32 : 4, SKH = S16 ? 4 : 4 * SROWS;
   const uint32_t saddr = lds0 + SC0 + (am + l32) * SROW + kh * SKH,
                  sbddr = lds0 + SC0 + (256 + bn + l32) * SROW + kh * SKH;
   auto load_quarter = [&](Quarter<MT>& f, auto stage, auto quarter) {
     constexpr int st = decltype(stage)::value, h = decltype(quarter)::value;
+    const uint32_t ah = fresh(aaddr) ^ (16 * h), bh = fresh(baddr) ^ (16 * h);
     static_for<JT>([&](auto j) {
-      f.b[decltype(j)::value] = lds_b128<st * OPB + decltype(j)::value * 4096>(baddr[h]);
+      f.b[decltype(j)::value] = lds_b128<st * OPB + decltype(j)::value * 4096>(bh);
     });
     static_for<MT>([&](auto i) {
-      f.a[decltype(i)::value] = lds_b128<st * OPB + decltype(i)::value * 4096>(aaddr[h]);
+      f.a[decltype(i)::value] = lds_b128<st * OPB + decltype(i)::value * 4096>(ah);
     });
   };
   auto load_scales = [&](Scales<MT>& f, int d) {
@@ -259,6 +256,7 @@ __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int
   // through the wavefront's strip of LDS so that a row's columns leave together;
   // the 16-byte granules are swizzled by row
   uint8_t* strip = smem + wave * STRIP;
+  const int le = (int)fresh(threadIdx.x & 63), e32 = le & 31, eh = le >> 5;
   auto fence = [] {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -274,21 +272,21 @@ __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const f32x16& v = acc[i][j];
-          *reinterpret_cast<u32x2*>(at(32 * i + l32, 4 * j + q) + 8 * kh) =
+          *reinterpret_cast<u32x2*>(at(32 * i + e32, 4 * j + q) + 8 * eh) =
               u32x2{bf16_pair(v[4 * q], v[4 * q + 1]), bf16_pair(v[4 * q + 2], v[4 * q + 3])};
         }
     fence();
 #pragma unroll
     for (int t = 0; t < 32 * MT * GR / 64; ++t) {
-      const int r = (64 / GR) * t + lane / GR, c = lane % GR;
+      const int r = (64 / GR) * t + le / GR, c = le % GR;
       const int m = m0 + am + r, n = n0 + bn + 8 * c;
       const u32x4 v = *reinterpret_cast<const u32x4*>(at(r, c));
       if (m < cnt && n < g.N)
         *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.out) + ((size_t)lo + m) * g.N + n) = v;
     }
   } else {
-    // fp32: 64 rows at a time
-    constexpr int GR = COLS / 4, R = MT < 2 ? 1 : 2;
+    // fp32: 64 rows (32 of an odd number of tiles) at a time
+    constexpr int GR = COLS / 4, R = MT % 2 ? 1 : 2;
     auto at = [&](int r, int c) { return strip + r * (4 * COLS) + ((c ^ (r & 15)) << 4); };
     static_for<MT / R>([&](auto hh) {
       constexpr int h = decltype(hh)::value;
@@ -299,13 +297,13 @@ __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f32x16& v = acc[R * h + i][j];
-            *reinterpret_cast<f32x4*>(at(32 * i + l32, 8 * j + 2 * q + kh)) =
+            *reinterpret_cast<f32x4*>(at(32 * i + e32, 8 * j + 2 * q + eh)) =
                 f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
           }
       fence();
 #pragma unroll
       for (int t = 0; t < 32 * R * GR / 64; ++t) {
-        const int r = (64 / GR) * t + lane / GR, c = lane % GR;
+        const int r = (64 / GR) * t + le / GR, c = le % GR;
         const int m = m0 + am + 32 * R * h + r, n = n0 + bn + 4 * c;
         const f32x4 v = *reinterpret_cast<const f32x4*>(at(r, c));
         if (m < cnt && n < g.N)
@@ -322,8 +320,10 @@ __global__ __launch_bounds__(64 * WAVES, 1) void mxfp4_tile_kernel(GroupedArgs g
   RowTile t;
   if (!find_tile<256, GM>(g, nt, t)) return;
   const int left = t.cnt - t.m0, n0 = BN * t.nt;
-  if (left > 128)
+  if (left > 192)
     mx_body<S16, BIG, 4>(g, smem, t.e, t.lo, t.cnt, t.m0, n0);
+  else if (left > 128)
+    mx_body<S16, BIG, 3>(g, smem, t.e, t.lo, t.cnt, t.m0, n0);
   else if (left > 64)
     mx_body<S16, BIG, 2>(g, smem, t.e, t.lo, t.cnt, t.m0, n0);
   else
@@ -334,7 +334,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void mxfp4_tile_kernel(GroupedArgs g
 
 hipError_t launch_mxfp4_tile(const GroupedArgs& a, hipStream_t st) {
   const int nt = (a.N + BN - 1) / BN, lanes = 64 * WAVES;
-  const long long n = (max_row_tiles(a.M, a.E, 256) * nt + 7) / 8 * 8;
+  const long long n = tile_grid(a, 256, nt);
   if (n * lanes >= (1LL << 32)) return hipErrorInvalidValue;
   // buffer offsets have 32 bits, and the codes are the larger part of a
   if (a.a_rows * (a.K / 2) > (long long)kOut)

@@ -28,11 +28,20 @@ enum GroupedLayout {
   G_NT = 1,  // w [E, N, K]
   G_TN = 2   // weight gradient
 };
-enum GroupedInput { G_BF16 = 0, G_F32 = 1, G_MX = 2 };
+enum GroupedInput { G_BF16 = 0, G_MX = 1 };
 
-// fp32 products of any input type on 64 x 64 tiles (the fp32 layer's path).
-hipError_t launch_grouped_simple(GroupedInput in, GroupedLayout lay, const GroupedArgs& a,
-                                 hipStream_t st);
+// Whether every launch below stays within 2^31 work items and 2^32 lanes: the
+// smallest row tile has 16 rows, the smallest column tile 64 columns, and a
+// workgroup of the streaming kernels up to 256 lanes (weight gradients: 64 x 64
+// tiles of 256 lanes).
+inline bool grouped_fits(long long M, int K, int N, int E) {
+  const long long cols = (N + 63) / 64, rows = M / 16 + (E < M ? E : M);
+  const long long wgrad = (long long)E * ((K + 63) / 64);
+  return rows * cols < (1 << 24) - 64 && wgrad < (1 << 24);
+}
+
+// fp32 products and weight gradients (the fp32 layer's path).
+hipError_t launch_grouped_simple(GroupedLayout lay, const GroupedArgs& a, hipStream_t st);
 
 // bf16 products and weight gradients on 256 x 256 tiles.
 hipError_t launch_grouped_tile(GroupedLayout lay, const GroupedArgs& a, hipStream_t st);

@@ -173,6 +173,78 @@ def test_bad_rows_stay_where_they_are(layout, per):
     assert not torch.isfinite(out[[1, per, M - 1]]).any()
 
 
+def wide_index(M, rows):
+    """Rows spread over the whole of a long array, its last one among them."""
+    idx = (torch.arange(M, dtype=torch.int64, device="cuda") * 7919 * 131) % rows
+    idx[-1] = rows - 1
+    return idx.to(torch.int32)
+
+
+@pytest.mark.parametrize("per,N", [(3, 72), (700, 16392)])
+@pytest.mark.parametrize("mx", [False, True])
+def test_rows_past_32_bits(mx, per, N):
+    """Gathered from arrays of more than 4 GiB, by the streaming and the tiled kernels."""
+    g, K = gen(8), 8192
+    rows = (1 << 20) + 4000 if mx else (1 << 18) + 4000
+    idx = wide_index(per, rows)
+    picked = idx.long().unique()
+    off, out = ref.offsets_of([0, per]), torch.empty(per, N, device="cuda")
+    w = normal(g, 2, N, K, scale=K ** -0.5)
+    if mx:
+        a = torch.zeros(rows, K // 2, dtype=torch.uint8, device="cuda")
+        sa = torch.full((rows, moe.moe_mxfp4_scale_stride(K)), 255, dtype=torch.uint8, device="cuda")
+        a[picked], sa[picked] = quantised(normal(g, picked.numel(), K))
+        cw, sw = quantised(w)
+        moe.moe_mxfp4_grouped_gemm(a, sa, cw, sw, off, out, row_index=idx)
+        x, w64 = ref.mx_decode64(a[idx.long()], sa[idx.long()]), ref.mx_decode64(cw, sw)
+    else:
+        a = torch.empty(rows, K, dtype=BF, device="cuda")
+        a[picked] = normal(g, picked.numel(), K)
+        moe.moe_grouped_gemm(a, w, off, out, row_index=idx, w_trans=True)
+        x, w64 = a[idx.long()].double(), w
+    want, mag = ref.product64(x, w64, [0, per], True)
+    close(out, want, ref.sum_bound(want, mag, K, F32))
+
+
+def test_results_past_32_bits():
+    """Rows of out, and of d, past the first 4 GiB."""
+    g, K, N, M = gen(9), 8, 1024, (1 << 20) + 4321
+    counts = [M - 700, 0, 700]
+    off, a, w = ref.offsets_of(counts), normal(g, M, K), normal(g, 3, K, N)
+    out = torch.empty(M, N, device="cuda")
+    moe.moe_grouped_gemm(a, w, off, out)
+    for lo in (0, M - 1400, M - 700):
+        e = 0 if lo < M - 700 else 2
+        want = a[lo:lo + 700].double() @ w[e].double()
+        close(out[lo:lo + 700], want, ref.sum_bound(want, a[lo:lo + 700].double().abs() @ w[e].double().abs(), K, F32))
+    d = torch.zeros(2 * M, N, dtype=BF, device="cuda")
+    d[-700:] = normal(g, 700, N)
+    a2 = torch.zeros(2 * M, K, dtype=BF, device="cuda")
+    a2[-700:] = normal(g, 700, K)
+    dw = torch.empty(3, K, N, device="cuda")
+    moe.moe_grouped_wgrad(a2, d, ref.offsets_of([2 * M - 700, 0, 700]), dw)
+    want, mag = ref.wgrad64(a2[-700:].double(), d[-700:], [700])
+    close(dw[2:], want, ref.sum_bound(want, mag, 700, F32))
+    assert not dw[:2].any()
+
+
+def test_two_row_indices_of_one_row():
+    """The same source row under many sorted rows, on both sides of an expert's border."""
+    g, K, N = gen(10), 64, 72
+    counts = [37, 91]
+    idx = torch.full((128,), 5, dtype=torch.int32, device="cuda")
+    a, w, d = normal(g, 9, K), normal(g, 2, K, N), normal(g, 128, N)
+    out, dw = torch.empty(128, N, device="cuda"), torch.empty(2, K, N, device="cuda")
+    off = ref.offsets_of(counts)
+    moe.moe_grouped_gemm(a, w, off, out, row_index=idx)
+    moe.moe_grouped_wgrad(a, d, off, dw, row_index=idx)
+    x = ref.gather64(a, 128, idx)
+    want, mag = ref.product64(x, w, counts, False)
+    close(out, want, ref.sum_bound(want, mag, K, F32))
+    want, mag = ref.wgrad64(x, d, counts)
+    close(dw, want, ref.sum_bound(want, mag, 91, F32))
+
+
 # ------------------------------------------------------------------ SwiGLU
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("M,I", [(1, 8), (3, 40), (129, 264), (1000, 1416)])
@@ -440,9 +512,10 @@ def test_serving_pass_mxfp4():
     close(b["out"], terms.sum(1), ref.sum_bound(terms.sum(1), terms.abs().sum(1), k + 1, BF))
 
 
-def test_streams_and_graph():
+@pytest.mark.parametrize("T,k,E,H,I", [(70, 3, 6, 128, 96), (1500, 4, 40, 320, 264)])
+def test_streams_and_graph(T, k, E, H, I):
     """Two passes side by side on two streams, and both captured and replayed among eager work."""
-    Ls = [layer(s, 70, 3, 6, 128, 96, BF) for s in (1, 2)]
+    Ls = [layer(s, T, k, E, H, I, BF) for s in (1, 2)]
     want = []
     for L in Ls:
         b = buffers(L)

@@ -38,7 +38,7 @@ def test_grouped_gemm_refusals():
                 dict(out=A), dict(out=A + 64 * 128 * 2 - 16), dict(out=B), dict(out=C), dict(out=F, idx=F + 64)):
         assert f(**bad) == INVAL, bad
     for bad in (dict(E=257), dict(K=100), dict(N=60), dict(M=1 << 29, a_rows=1 << 29), dict(a_rows=1 << 31),
-                dict(K=(1 << 20) + 8), dict(N=(1 << 20) + 8)):
+                dict(K=(1 << 20) + 8), dict(N=(1 << 20) + 8), dict(M=1 << 26, a_rows=1 << 26, N=512)):
         assert f(**bad) == UNSUP, bad
 
 
@@ -106,7 +106,8 @@ def test_mxfp4_grouped_gemm_refusals():
                 dict(a=MIS), dict(asc=MIS), dict(wsc=MIS), dict(odt=2), dict(a_rows=63), dict(idx=C, div=0),
                 dict(out=A), dict(out=B), dict(out=C), dict(out=D), dict(out=F)):
         assert f(**bad) == INVAL, bad
-    for bad in (dict(K=48), dict(N=4), dict(E=257), dict(M=1 << 29, a_rows=1 << 29)):
+    for bad in (dict(K=48), dict(N=4), dict(E=257), dict(M=1 << 29, a_rows=1 << 29),
+                dict(a_rows=1 << 30)):
         assert f(**bad) == UNSUP, bad
 
 
