@@ -13,6 +13,12 @@
 // Fragments, swizzles and zeros outside the operands as in grouped_tile.hip; the
 // MFMA is 16x16x32 bf16, or the block-scaled 16x16x128 for MXFP4 (lane l: row
 // l % 16, block l / 16 of four).
+//
+// Measured at K = 5120, N = 1536: one token through 8 of 256 bf16 experts 25 us
+// (w [N, K] 22 us; 5 us without the weights, then 6.4 TB/s), 64 tokens 474 us (7.4
+// TB/s); MXFP4, 16 tokens, 71 us (6.0 TB/s; 94 us with 64-byte pieces and a load
+// per scale and step). The rings in flight, not their depth, set the rate: six or
+// eight wavefronts per CU with two to four stages are within 3%.
 #include "grouped_common.h"
 
 namespace moe {

@@ -5,7 +5,8 @@
 // One workgroup of 8 wavefronts (2 x 4) computes a 256 x 256 tile of one
 // expert, 128 x 64 per wavefront (8 x 4 MFMA 16x16x32 tiles, 128 accumulators);
 // an expert's last tile of at most 192, 128 or 64 rows keeps 96, 64 or 32 rows
-// per wavefront, so that short experts pay for their weights, not for padding.
+// per wavefront, so that short experts pay for their weights, not for padding
+// (160 rows per expert: 405 us, 412 us without the 192).
 // The depth advances 64 at a time (a pair of 32-deep steps); LDS holds five
 // such pairs of the operands, filled by direct global -> LDS loads. An operand
 // whose rows are contiguous along the depth comes in as 128-byte rows and is
@@ -20,9 +21,21 @@
 // with zero); gathered rows are addressed per lane.
 //
 // A step: half of the row fragments and all column fragments are in registers;
-// read the other half while the first MFMAs run; wait, meet the others, refill
-// what was just consumed, and read the next step's fragments while the other
-// MFMAs run. Every LDS wait is for reads a block of MFMAs ago.
+// read the other half while the first MFMAs run; wait (after a pair's second step
+// also for the others and the next pair), then read the next step's fragments and
+// refill the pair just consumed while the other MFMAs run. Every LDS wait is for
+// reads a block of MFMAs ago.
+//
+// Measured: 65536 rows x 5120 x 2560 over 64 uneven experts 1.59 ms (1.08
+// PFLOP/s; w [N, K] 1.54 ms), over 8 experts 1.42 ms (1.21); a library product of
+// one large matrix runs at 1.36. Without its loads it takes 1.16 ms, without its
+// MFMAs 1.12, without both 0.53, the MFMAs alone 0.94: no single part bounds it,
+// what remains is how far they overlap between barriers. The weight gradient
+// 64 x 5120 x 1536 over 32768 rows takes 0.84 ms, its 2 GB of fp32 results and
+// the short sums (16 steps a tile) weighing most. Two workgroups of 256 x 128 per
+// CU were 20% slower, four wavefronts of 128 x 128 spill, and one workgroup per CU
+// that loads the next tile during its epilogue was 15% slower (3% faster for the
+// weight gradient): dropped.
 // The MFMA takes the column operand first, so that a lane ends with four
 // adjacent columns of a row and the epilogue packs them without shuffles.
 #include "grouped_common.h"
@@ -150,6 +163,15 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, uint8_t* smem, i
   // weight gradient: the source rows of this wavefront's eight depth rows of
   // pair p (p % 64 = lane), refreshed every 64 pairs
   int src[8];
+  auto refresh = [&](int p) {
+    if (LAY == G_TN && (p & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 64 * (p + lane) + 8 * wave + i;
+        src[i] = r < cnt ? source_row(g, lo + r) : -1;
+      }
+    }
+  };
   // loads of pair p of a into slot `slot`
   auto issue_a = [&](int p, int slot) {
     uint8_t* to = smem + slot * PAIR + wave * (LA * 1024);
@@ -158,13 +180,6 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, uint8_t* smem, i
       for (int q = 0; q < LA; ++q)
         dma16(p < alim[q] ? ap[q] + (size_t)p * 128 : zeros, to + q * 1024);
     } else {
-      if ((p & 63) == 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 64 * (p + lane) + 8 * wave + i;
-          src[i] = r < cnt ? source_row(g, lo + r) : -1;
-        }
-      }
 #pragma unroll
       for (int q = 0; q < LA; ++q) {
         const int s0 = __builtin_amdgcn_readlane(src[2 * q], p & 63);
@@ -251,6 +266,7 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, uint8_t* smem, i
   if (np > 0) {
     // in the order in which the loop refills, so that a wait for all but the
     // last loads is a wait for the pair
+    refresh(0);
     if constexpr (LAY == G_TN) {
       issue_b(0, 0), issue_a(0, 0), issue_b(1, 1), issue_a(1, 1), issue_a(2, 2);
       wait_loads<2 * LA + LB>();  // pair 0 has landed
@@ -286,15 +302,21 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, uint8_t* smem, i
       front(c1, b1);
       // the next pair has landed (all but the loads of the longer ring's pair
       // after it), for everyone after the barrier, and everyone has read this
-      // pair: refill it
+      // pair: refill it, in the shadow of the MFMAs
       wait_loads<LAY == G_TN ? LA : LB>();
       __builtin_amdgcn_s_barrier();
-      if constexpr (LAY == G_TN) issue_b(p + NSB, sb);
-      issue_a(p + NSA, sa);
-      if constexpr (LAY != G_TN) issue_b(p + NSB, sb);
+      refresh(p + NSA);
+      const int ra = sa, rb = sb;
       sa = sa == NSA - 1 ? 0 : sa + 1;
       sb = sb == NSB - 1 ? 0 : sb + 1;
-      back(c0, b1, b0);
+      load_b(b0, sb * PAIR, c0);
+      load_a(a0, sa * PAIR, c0, c0);
+      if constexpr (LAY == G_TN) issue_b(p + NSB, rb);
+      issue_a(p + NSA, ra);
+      if constexpr (LAY != G_TN) issue_b(p + NSB, rb);
+      mfmas(a1, b1, c1);
+      wait_frags(b0);
+      wait_frags(a0);
     }
     wait_loads<0>();
   }
