@@ -118,7 +118,7 @@ __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int
     const int row = S16 ? 64 * QS * (wave & 3) + 32 * q + (lane >> 1) : 64 * (QS * (wave & 3) + q) + lane;
     int r = row;
     if (wave < 4) r = (row < 64 * MT && m0 + row < cnt) ? source_row(g, lo + m0 + row) : -1;
-    srow[q] = (r < 0 ? kOut : (uint32_t)r * (uint32_t)g.S) + (S16 ? 16 * (lane & 1) : 0);
+    srow[q] = (r < 0 ? kOut : (uint32_t)r * (uint32_t)g.S) + (S16 ? 16 * ((lane & 1) ^ ((lane >> 4) & 1)) : 0);
   }
   const Buffer sbuf = wave < 4 ? make_buffer(g.a_scale, (uint32_t)g.a_rows * (uint32_t)g.S)
                                : make_buffer(g.w_scale + ((size_t)e * g.N + n0) * g.S, (uint32_t)wrows * (uint32_t)g.S);
@@ -163,9 +163,11 @@ __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int
   // granule 4 kh + h sits h << 4 away from granule 4 kh, in the XOR sense
   const int gr0 = ((4 * kh) ^ swz_row(l32)) << 4;
   const uint32_t aaddr = lds0 + (am + l32) * 128 + gr0, baddr = lds0 + NST * OPB + (bn + l32) * 128 + gr0;
+  // S16: a row's two 16-byte halves are swapped in every other block of eight rows,
+  // so that the dwords of 32 rows meet in pairs in the banks, not in fours
   constexpr int SROW = S16 ? 32 : 4, SKH = S16 ? 4 : 4 * SROWS;
-  const uint32_t saddr = lds0 + SC0 + (am + l32) * SROW + kh * SKH,
-                 sbddr = lds0 + SC0 + (256 + bn + l32) * SROW + kh * SKH;
+  const int swap = S16 ? 16 * ((l32 >> 3) & 1) : 0;
+  const uint32_t saddr = SC0 + (am + l32) * SROW + kh * SKH + swap, sbddr = SC0 + (256 + bn + l32) * SROW + kh * SKH + swap;
   auto load_quarter = [&](Quarter<MT>& f, auto stage, auto quarter) {
     constexpr int st = decltype(stage)::value, h = decltype(quarter)::value;
     const uint32_t ah = fresh(aaddr) ^ (16 * h), bh = fresh(baddr) ^ (16 * h);
@@ -177,12 +179,15 @@ __device__ __forceinline__ void mx_body(const GroupedArgs& g, uint8_t* smem, int
     });
   };
   auto load_scales = [&](Scales<MT>& f, int d) {
-    const uint32_t off = ((d >> 2) & 1) * SCB + (d & 3) * 2 * SKH;
+    // stage d % 4 of the chunk: bytes 8 (d % 4) of the row, or planes 2 (d % 4), + 1
+    const uint32_t off = lds0 + ((d >> 2) & 1) * SCB + (S16 ? (d & 1) * 8 : (d & 3) * 2 * SKH);
+    const int half = S16 ? 8 * (d & 2) : 0;
+    const uint32_t sa = (saddr ^ half) + off, sb = (sbddr ^ half) + off;
     static_for<JT>([&](auto j) {
-      f.b[decltype(j)::value] = lds_b32<decltype(j)::value * 32 * SROW>(sbddr + off);
+      f.b[decltype(j)::value] = lds_b32<decltype(j)::value * 32 * SROW>(sb);
     });
     static_for<MT>([&](auto i) {
-      f.a[decltype(i)::value] = lds_b32<decltype(i)::value * 32 * SROW>(saddr + off);
+      f.a[decltype(i)::value] = lds_b32<decltype(i)::value * 32 * SROW>(sa);
     });
   };
   // scale bytes past K / 32 are no scales: zero (their codes are zeros)
