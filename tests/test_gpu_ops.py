@@ -66,6 +66,9 @@ SHAPES = [
     ([300, 31, 600], 64, 16392),
     # one long expert among short ones: the streaming kernels
     ([300] + [0, 1] * 40, 320, 200),
+    # as many experts as there may be
+    ([0, 1, 2, 3] * 64, 96, 72),
+    ([40, 0, 17, 90] * 64, 64, 72),
 ]
 
 
@@ -394,6 +397,19 @@ def test_mxfp4_grouped_gemm(case, out_dtype):
     want, mag = ref.product64(x, w64, counts, True)
     close(out[:used], want, ref.sum_bound(want, mag, K, out_dtype))
     assert bool((out[used:] == 7.0).all()) and ref.guards_intact(big, 16, 7.0)
+
+
+@pytest.mark.parametrize("K", [8192, 12800, 13312])
+@pytest.mark.parametrize("counts", [[3, 0, 2], [40, 60]])
+def test_mxfp4_long_depth(K, counts):
+    """Depths whose scales fill the streaming kernels' LDS, and one past that."""
+    g, E, N, M = gen(K), len(counts), 72, sum(counts)
+    ca, sa = quantised(normal(g, M, K))
+    cw, sw = quantised(normal(g, E, N, K, scale=K ** -0.5))
+    out = torch.empty(M, N, device="cuda")
+    moe.moe_mxfp4_grouped_gemm(ca, sa, cw, sw, ref.offsets_of(counts), out)
+    want, mag = ref.product64(ref.mx_decode64(ca, sa), ref.mx_decode64(cw, sw), counts, True)
+    close(out, want, ref.sum_bound(want, mag, K, F32))
 
 
 # ------------------------------------------------------------------ together
