@@ -315,41 +315,61 @@ def moe_forward_noalloc(x, w_router, bias, w: ExpertWeights, I: int, k: int, out
 
 
 # ---------------------------------------------------------------- operators around the layer
+# A small call is bound by its host side, so these check in line and touch each tensor once.
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() builds an object: 2.7 us a call
+_current_device = torch._C._cuda_getDevice
+_FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
-def _call(fn: str, tensors, stream, *args):
-    """One call of the C ABI on the tensors' own device (all on one GPU), on the
-    given stream or that device's current one."""
-    index = -1
+def _refuse(fn: str, what: str):
+    raise ValueError(f"{fn}: {what}")
+
+
+def _float(t: torch.Tensor) -> int:
+    d = _FLOATS.get(t.dtype)
+    return _dt(t) if d is None else d  # _dt raises
+
+
+def _arrays(fn: str, tensors):
+    """Addresses of tensors (None for None), all contiguous and on one GPU, and that GPU's index."""
+    index, at = None, []
     for t in tensors:
-        if t is not None:
-            d = t.get_device()
+        if t is None:
+            at.append(None)
+            continue
+        d = t.get_device()
+        if d != index:
             if d < 0:
-                raise ValueError(f"{fn} takes device tensors")
-            if index < 0:
-                index = d
-            elif d != index:
-                raise ValueError(f"{fn}: tensors on different devices")
+                _refuse(fn, "takes device tensors")
+            if index is not None:
+                _refuse(fn, "tensors on different devices")
+            index = d
+        if not t.is_contiguous():
+            _refuse(fn, "tensors must be contiguous")
+        at.append(t.data_ptr())
+    return index, at
+
+
+def _run(fn: str, call, index: int, stream, *args):
+    """One call of the C ABI on GPU `index`, on the given stream or that GPU's current one."""
     raw = _raw_stream(index) if stream is None else _stream(stream)
-    if index == torch.cuda.current_device():
-        _check(fn, getattr(_lib, fn)(*args, raw))
+    if index == _current_device():
+        status = call(*args, raw)
     else:
         with torch.cuda.device(index):
-            _check(fn, getattr(_lib, fn)(*args, raw))
+            status = call(*args, raw)
+    if status:
+        raise MoEError(fn, status)
 
 
-def _need(fn: str, ok: bool, what: str):
-    if not ok:
-        raise ValueError(f"{fn}: {what}")
-
-
-def _rows_args(fn, M, E, offsets, row_index, row_div):
-    if offsets.dtype != torch.int32 or offsets.shape != (E + 1,):
-        raise ValueError(f"{fn}: offsets must be int32 [E + 1]")
+def _check_rows(fn, M, E, offsets, row_index, row_div):
+    if offsets.dtype is not torch.int32 or offsets.shape != (E + 1,):
+        _refuse(fn, "offsets must be int32 [E + 1]")
     if row_index is not None:
-        _need(fn, row_index.dtype == torch.int32 and row_index.numel() == M, "row_index must be int32 [M]")
-        _need(fn, row_div >= 1, "row_div must be positive")
+        if row_index.dtype is not torch.int32 or row_index.numel() != M:
+            _refuse(fn, "row_index must be int32 [M]")
+        if row_div < 1:
+            _refuse(fn, "row_div must be positive")
 
 
 def moe_grouped_gemm(a, w, offsets, out, row_index=None, row_div: int = 1, w_trans: bool = False,
@@ -358,13 +378,19 @@ def moe_grouped_gemm(a, w, offsets, out, row_index=None, row_div: int = 1, w_tra
     moe_permute writes them). a [rows, K], w [E, K, N] (w_trans: [E, N, K]), out [M, N]. The
     input gradient is the same call on the output gradient with w_trans flipped."""
     fn = "moe_grouped_gemm"
-    _need(fn, a.dim() == 2 and w.dim() == 3 and out.dim() == 2, "a and out are matrices, w [E, ., .]")
-    (rows, K), (M, N), E = a.shape, out.shape, w.shape[0]
-    _need(fn, w.shape[1:] == ((N, K) if w_trans else (K, N)), "shapes of a, w and out do not match")
-    _need(fn, w.dtype == a.dtype, "a and w must have one dtype")
-    _rows_args(fn, M, E, offsets, row_index, row_div)
-    _call(fn, (a, w, offsets, out, row_index), stream, _ptr(a), _dt(a), rows, _ptr(row_index),
-          row_div, _ptr(w), int(w_trans), M, K, N, E, _ptr(offsets), _dt(out), _ptr(out))
+    sa, sw, so = a.shape, w.shape, out.shape
+    if len(sa) != 2 or len(sw) != 3 or len(so) != 2:
+        _refuse(fn, "a and out are matrices, w [E, ., .]")
+    (rows, K), (M, N), E = sa, so, sw[0]
+    if sw != ((E, N, K) if w_trans else (E, K, N)):
+        _refuse(fn, "shapes of a, w and out do not match")
+    if w.dtype is not a.dtype:
+        _refuse(fn, "a and w must have one dtype")
+    _check_rows(fn, M, E, offsets, row_index, row_div)
+    t_in, t_out = _float(a), _float(out)
+    dev, (pa, pw, po, pout, pi) = _arrays(fn, (a, w, offsets, out, row_index))
+    _run(fn, _lib.moe_grouped_gemm, dev, stream, pa, t_in, rows, pi, row_div, pw,
+         1 if w_trans else 0, M, K, N, E, po, t_out, pout)
 
 
 def moe_grouped_wgrad(a, d, offsets, dw, row_index=None, row_div: int = 1, accumulate: bool = False,
@@ -372,52 +398,70 @@ def moe_grouped_wgrad(a, d, offsets, dw, row_index=None, row_div: int = 1, accum
     """dw[e] = sum over expert e's rows r of a[row_index[r] // row_div]^T d[r] (accumulate: added
     to dw, fp32). a [rows, K], d [M, N], dw [E, K, N]."""
     fn = "moe_grouped_wgrad"
-    _need(fn, a.dim() == 2 and d.dim() == 2 and dw.dim() == 3, "a and d are matrices, dw [E, K, N]")
-    (rows, K), (M, N), E = a.shape, d.shape, dw.shape[0]
-    _need(fn, dw.shape[1:] == (K, N), "shapes of a, d and dw do not match")
-    _need(fn, a.dtype == d.dtype, "a and d must have one dtype")
-    _rows_args(fn, M, E, offsets, row_index, row_div)
-    _call(fn, (a, d, offsets, dw, row_index), stream, _ptr(a), _dt(a), rows, _ptr(row_index),
-          row_div, _ptr(d), M, K, N, E, _ptr(offsets), _dt(dw), int(accumulate), _ptr(dw))
+    sa, sd, sw = a.shape, d.shape, dw.shape
+    if len(sa) != 2 or len(sd) != 2 or len(sw) != 3:
+        _refuse(fn, "a and d are matrices, dw [E, K, N]")
+    (rows, K), (M, N), E = sa, sd, sw[0]
+    if sw != (E, K, N):
+        _refuse(fn, "shapes of a, d and dw do not match")
+    if a.dtype is not d.dtype:
+        _refuse(fn, "a and d must have one dtype")
+    _check_rows(fn, M, E, offsets, row_index, row_div)
+    t_in, t_out = _float(a), _float(dw)
+    dev, (pa, pd, po, pw, pi) = _arrays(fn, (a, d, offsets, dw, row_index))
+    _run(fn, _lib.moe_grouped_wgrad, dev, stream, pa, t_in, rows, pi, row_div, pd, M, K, N, E,
+         po, t_out, 1 if accumulate else 0, pw)
 
 
 def moe_swiglu(a, h, stream=None):
     """h = silu(a[:, :I]) * a[:, I:]; a [M, 2I], h [M, I], bf16 or fp32."""
     fn = "moe_swiglu"
-    _need(fn, h.dim() == 2 and a.shape == (h.shape[0], 2 * h.shape[1]),
-          "a must be [M, 2I] and h [M, I]")
-    _need(fn, a.dtype == h.dtype, "a and h must have one dtype")
-    _call(fn, (a, h), stream, _ptr(a), _dt(a), h.shape[0], h.shape[1], _ptr(h))
+    sh = h.shape
+    if len(sh) != 2 or a.shape != (sh[0], 2 * sh[1]):
+        _refuse(fn, "a must be [M, 2I] and h [M, I]")
+    if a.dtype is not h.dtype:
+        _refuse(fn, "a and h must have one dtype")
+    t_in = _float(a)
+    dev, (pa, ph) = _arrays(fn, (a, h))
+    _run(fn, _lib.moe_swiglu, dev, stream, pa, t_in, sh[0], sh[1], ph)
 
 
 def moe_swiglu_backward(a, dh, da, h=None, stream=None):
     """da [M, 2I] = gradient of moe_swiglu at a for dh [M, I]; h [M, I], if given, is formed again.
     da may be a and h may be dh."""
     fn = "moe_swiglu_backward"
-    _need(fn, dh.dim() == 2 and a.shape == (dh.shape[0], 2 * dh.shape[1]),
-          "a must be [M, 2I] and dh [M, I]")
-    _need(fn, da.shape == a.shape and (h is None or h.shape == dh.shape), "da is shaped as a, h as dh")
-    _need(fn, all(t is None or t.dtype == a.dtype for t in (dh, da, h)), "all tensors must have one dtype")
-    _call(fn, (a, dh, da, h), stream, _ptr(a), _ptr(dh), _dt(a), dh.shape[0], dh.shape[1], _ptr(da),
-          _ptr(h))
+    sh, t = dh.shape, a.dtype
+    if len(sh) != 2 or a.shape != (sh[0], 2 * sh[1]):
+        _refuse(fn, "a must be [M, 2I] and dh [M, I]")
+    if da.shape != a.shape or (h is not None and h.shape != sh):
+        _refuse(fn, "da is shaped as a, h as dh")
+    if dh.dtype is not t or da.dtype is not t or (h is not None and h.dtype is not t):
+        _refuse(fn, "all tensors must have one dtype")
+    t_in = _float(a)
+    dev, (pa, pdh, pda, ph) = _arrays(fn, (a, dh, da, h))
+    _run(fn, _lib.moe_swiglu_backward, dev, stream, pa, pdh, t_in, sh[0], sh[1], pda, ph)
 
 
 def moe_finalize_backward(dout, y_sorted, pair_pos, topk_w, dy_sorted, dtopk_w, stream=None):
     """Gradients of moe_finalize: dy_sorted[pair_pos] = topk_w * dout, dtopk_w = <dout, y_sorted[pair_pos]>
     (either output may be None; y_sorted may be None without dtopk_w)."""
     fn = "moe_finalize_backward"
-    _need(fn, dout.dim() == 2 and topk_w.dim() == 2, "dout must be [T, H] and topk_w [T, k]")
-    (T, H), k = dout.shape, topk_w.shape[1]
-    _need(fn, topk_w.shape[0] == T and topk_w.dtype == torch.float32, "topk_w must be fp32 [T, k]")
-    _need(fn, pair_pos.dtype == torch.int32 and pair_pos.numel() == T * k, "pair_pos must be int32 [T*k]")
-    _need(fn, y_sorted is None or (y_sorted.dtype == torch.float32 and y_sorted.shape == (T * k, H)),
-          "y_sorted must be fp32 [T*k, H]")
-    _need(fn, dy_sorted is None or dy_sorted.shape == (T * k, H), "dy_sorted must be [T*k, H]")
-    _need(fn, dtopk_w is None or (dtopk_w.dtype == torch.float32 and dtopk_w.shape == topk_w.shape),
-          "dtopk_w must be fp32 [T, k]")
-    _call(fn, (dout, y_sorted, pair_pos, topk_w, dy_sorted, dtopk_w), stream, _ptr(dout), _dt(dout),
-          _ptr(y_sorted), _ptr(pair_pos), _ptr(topk_w), T, k, H,
-          MOE_F32 if dy_sorted is None else _dt(dy_sorted), _ptr(dy_sorted), _ptr(dtopk_w))
+    sd, sw = dout.shape, topk_w.shape
+    if len(sd) != 2 or len(sw) != 2 or sw[0] != sd[0] or topk_w.dtype is not torch.float32:
+        _refuse(fn, "dout must be [T, H] and topk_w fp32 [T, k]")
+    (T, H), k = sd, sw[1]
+    if pair_pos.dtype is not torch.int32 or pair_pos.numel() != T * k:
+        _refuse(fn, "pair_pos must be int32 [T*k]")
+    if y_sorted is not None and (y_sorted.dtype is not torch.float32 or y_sorted.shape != (T * k, H)):
+        _refuse(fn, "y_sorted must be fp32 [T*k, H]")
+    if dy_sorted is not None and dy_sorted.shape != (T * k, H):
+        _refuse(fn, "dy_sorted must be [T*k, H]")
+    if dtopk_w is not None and (dtopk_w.dtype is not torch.float32 or dtopk_w.shape != sw):
+        _refuse(fn, "dtopk_w must be fp32 [T, k]")
+    t_in, t_out = _float(dout), MOE_F32 if dy_sorted is None else _float(dy_sorted)
+    dev, (pd, py, pp, pw, pdy, pdw) = _arrays(fn, (dout, y_sorted, pair_pos, topk_w, dy_sorted, dtopk_w))
+    _run(fn, _lib.moe_finalize_backward, dev, stream, pd, t_in, py, pp, pw, T, k, H,
+         t_out, pdy, pdw)
 
 
 def moe_mxfp4_scale_stride(K: int) -> int:
@@ -425,32 +469,42 @@ def moe_mxfp4_scale_stride(K: int) -> int:
     return _lib.moe_mxfp4_scale_stride(K)
 
 
-def _mx_args(fn, codes, scales, rows, K):
-    if K % 32 != 0 or codes.dtype != torch.uint8 or codes.shape != (*rows, K // 2):
-        raise ValueError(f"{fn}: codes must be uint8 [rows, K/2], K a multiple of 32")
-    if scales.dtype != torch.uint8 or scales.shape != (*rows, (K // 32 + 3) // 4 * 4):
-        raise ValueError(f"{fn}: scales must be uint8 [rows, moe_mxfp4_scale_stride(K)]")
+def _check_mx(fn, codes, scales, rows, K):
+    if K % 32 or codes.dtype is not torch.uint8 or codes.shape != (*rows, K // 2):
+        _refuse(fn, "codes must be uint8 [rows, K/2], K a multiple of 32")
+    if scales.dtype is not torch.uint8 or scales.shape != (*rows, (K // 32 + 3) // 4 * 4):
+        _refuse(fn, "scales must be uint8 [rows, moe_mxfp4_scale_stride(K)]")
 
 
 def moe_mxfp4_quantize(x, codes, scales, trans: bool = False, stream=None):
     """MXFP4 of x [..., K] along its last dimension: codes [..., K/2], scales [..., S]. With trans,
     x [B, K, C] (or [K, C]) along its middle dimension: codes [B, C, K/2], scales [B, C, S]."""
     fn = "moe_mxfp4_quantize"
-    _need(fn, x.dim() in (2, 3), "x must have two or three dimensions")
-    B, R, C = x.shape if x.dim() == 3 else (1, *x.shape)
-    rows = (C,) if trans else (R,)
-    _mx_args(fn, codes, scales, (B, *rows) if x.dim() == 3 else rows, R if trans else C)
-    _call(fn, (x, codes, scales), stream, _ptr(x), _dt(x), int(trans), B, R, C, _ptr(codes), _ptr(scales))
+    sx = x.shape
+    if len(sx) == 2:
+        B, (R, C) = 1, sx
+        _check_mx(fn, codes, scales, (C,) if trans else (R,), R if trans else C)
+    elif len(sx) == 3:
+        B, R, C = sx
+        _check_mx(fn, codes, scales, (B, C) if trans else (B, R), R if trans else C)
+    else:
+        _refuse(fn, "x must have two or three dimensions")
+    t_in = _float(x)
+    dev, (px, pc, ps) = _arrays(fn, (x, codes, scales))
+    _run(fn, _lib.moe_mxfp4_quantize, dev, stream, px, t_in, 1 if trans else 0, B, R, C, pc, ps)
 
 
 def moe_mxfp4_dequantize(codes, scales, out, stream=None):
     """out [..., K] (bf16 or fp32) = the values of codes [..., K/2] under scales [..., S]."""
     fn = "moe_mxfp4_dequantize"
-    _need(fn, out.dim() >= 1, "out must be [..., K]")
-    K = out.shape[-1]
-    _mx_args(fn, codes, scales, out.shape[:-1], K)
-    _call(fn, (codes, scales, out), stream, _ptr(codes), _ptr(scales), out.numel() // max(K, 1), K,
-          _dt(out), _ptr(out))
+    so = out.shape
+    if not so:
+        _refuse(fn, "out must be [..., K]")
+    K = so[-1]
+    _check_mx(fn, codes, scales, so[:-1], K)
+    t_out = _float(out)
+    dev, (pc, ps, po) = _arrays(fn, (codes, scales, out))
+    _run(fn, _lib.moe_mxfp4_dequantize, dev, stream, pc, ps, out.numel() // max(K, 1), K, t_out, po)
 
 
 def moe_mxfp4_grouped_gemm(a_codes, a_scales, w_codes, w_scales, offsets, out, row_index=None,
@@ -458,15 +512,18 @@ def moe_mxfp4_grouped_gemm(a_codes, a_scales, w_codes, w_scales, offsets, out, r
     """moe_grouped_gemm of MXFP4 rows a ([rows, K/2] codes, [rows, S] scales) and weights
     ([E, N, K/2], [E, N, S]); out [M, N] bf16 or fp32."""
     fn = "moe_mxfp4_grouped_gemm"
-    _need(fn, a_codes.dim() == 2 and w_codes.dim() == 3 and out.dim() == 2,
-          "a_codes and out are matrices, w_codes [E, N, K/2]")
-    (rows, K2), (M, N), E = a_codes.shape, out.shape, w_codes.shape[0]
-    _mx_args(fn, a_codes, a_scales, (rows,), 2 * K2)
-    _mx_args(fn, w_codes, w_scales, (E, N), 2 * K2)
-    _rows_args(fn, M, E, offsets, row_index, row_div)
-    _call(fn, (a_codes, a_scales, w_codes, w_scales, offsets, out, row_index), stream, _ptr(a_codes),
-          _ptr(a_scales), rows, _ptr(row_index), row_div, _ptr(w_codes), _ptr(w_scales), M, 2 * K2, N,
-          E, _ptr(offsets), _dt(out), _ptr(out))
+    sa, sw, so = a_codes.shape, w_codes.shape, out.shape
+    if len(sa) != 2 or len(sw) != 3 or len(so) != 2:
+        _refuse(fn, "a_codes and out are matrices, w_codes [E, N, K/2]")
+    (rows, half), (M, N), E = sa, so, sw[0]
+    _check_mx(fn, a_codes, a_scales, (rows,), 2 * half)
+    _check_mx(fn, w_codes, w_scales, (E, N), 2 * half)
+    _check_rows(fn, M, E, offsets, row_index, row_div)
+    t_out = _float(out)
+    dev, (pa, psa, pw, psw, po, pout, pi) = _arrays(
+        fn, (a_codes, a_scales, w_codes, w_scales, offsets, out, row_index))
+    _run(fn, _lib.moe_mxfp4_grouped_gemm, dev, stream, pa, psa, rows, pi, row_div, pw, psw, M,
+         2 * half, N, E, po, t_out, pout)
 
 
 # ---------------------------------------------------------------- device plumbing
