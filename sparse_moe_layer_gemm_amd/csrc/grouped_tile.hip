@@ -31,11 +31,11 @@
 // one large matrix runs at 1.36. Without its loads it takes 1.16 ms, without its
 // MFMAs 1.12, without both 0.53, the MFMAs alone 0.94: no single part bounds it,
 // what remains is how far they overlap between barriers. The weight gradient
-// 64 x 5120 x 1536 over 32768 rows takes 0.84 ms, its 2 GB of fp32 results and
+// 64 x 5120 x 1536 over 32768 rows takes 0.84-0.88 ms, its 2 GB of fp32 results and
 // the short sums (16 steps a tile) weighing most. Two workgroups of 256 x 128 per
 // CU were 20% slower, four wavefronts of 128 x 128 spill, and one workgroup per CU
-// that loads the next tile during its epilogue was 15% slower (3% faster for the
-// weight gradient): dropped.
+// that loads the next tile during its epilogue was 10-15% slower (3% faster for
+// the weight gradient): dropped.
 // The MFMA takes the column operand first, so that a lane ends with four
 // adjacent columns of a row and the epilogue packs them without shuffles.
 #include "grouped_common.h"
