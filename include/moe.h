@@ -348,7 +348,7 @@ moe_status moe_swiglu_backward(const void* a, const void* dh, int32_t dtype, int
  * MOE_F32); y_sorted [T*k, H] f32 as moe_finalize reads it; either output may
  * be NULL (y_sorted may be NULL without dtopk_w), not both. A pair_pos from
  * T*k on counts as negative; no two pairs may have the same row. 1 <= k <= 8,
- * H a multiple of 64, 0 <= T < 2^24 (0: a no-op). The token
+ * H a multiple of 64 up to 2^30, 0 <= T < 2^24 (0: a no-op). The token
  * gradient of the expert rows is moe_finalize itself with weights of one. */
 moe_status moe_finalize_backward(const void* dout, int32_t dout_dtype, const float* y_sorted,
                                  const int32_t* pair_pos, const float* topk_w, int64_t T,

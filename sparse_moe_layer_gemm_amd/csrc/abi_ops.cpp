@@ -19,6 +19,7 @@ constexpr int64_t kMaxBytes = int64_t(1) << 46;  // no array is larger than the 
 constexpr int64_t kMaxScales = 0xFFF00000ll;       // bytes of a's MXFP4 scales (32-bit buffer offsets)
 constexpr int64_t kMaxLanes = (int64_t(1) << 32) - 1;  // lanes of one grid dimension
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
+constexpr int32_t kMaxHidden = 1 << 30;  // the finalize gradient's columns stay below 2^31
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 moe_status launch_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH; }
@@ -148,7 +149,7 @@ moe_status moe_finalize_backward(const void* dout, int32_t dout_dtype, const flo
                                  float* dtopk_w, void* stream) {
   if (!is_float(dout_dtype) || !is_float(dy_dtype)) return MOE_ERR_INVALID_ARGUMENT;
   if (T < 0 || k <= 0 || H <= 0) return MOE_ERR_INVALID_ARGUMENT;
-  if (k > 8 || H % 64 != 0 || T >= kMaxTokens) return MOE_ERR_UNSUPPORTED;
+  if (k > 8 || H % 64 != 0 || H > kMaxHidden || T >= kMaxTokens) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!dy_sorted && !dtopk_w) return MOE_ERR_INVALID_ARGUMENT;
   if (!array_ok(dout) || !array_ok(pair_pos) || !array_ok(topk_w) || !aligned16(dy_sorted) ||

@@ -79,6 +79,13 @@ def test_finalize_backward_refusals():
         assert f(**bad) == UNSUP, bad
 
 
+def test_finalize_backward_widest_row():
+    # a lane's column index runs 8192 past H: 2^31 - 64 would wrap
+    args = dict(dout=A, dt=1, y=B, pp=C, w=D, T=1, k=1, H=(1 << 30) + 64, ydt=1, dy=F, dw=G, st=None)
+    assert call("moe_finalize_backward", args) == UNSUP
+    assert call("moe_finalize_backward", dict(args, H=(1 << 31) - 64)) == UNSUP
+
+
 def test_mxfp4_refusals():
     lib = moe.load_library()
     assert [lib.moe_mxfp4_scale_stride(K) for K in (32, 128, 160, 5120, 48, 0, -32)] == [4, 4, 8, 160, 0, 0, 0]
