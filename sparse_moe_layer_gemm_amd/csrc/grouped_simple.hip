@@ -45,6 +45,7 @@ __global__ __launch_bounds__(256) void grouped_simple_kernel(GroupedArgs g) {
     e = blockIdx.x / mt;
     m0 = (blockIdx.x - e * mt) * BT;
     expert_rows(g.offsets, e, g.M, lo, cnt);
+    if (g.accumulate && cnt == 0) return;  // dw keeps what it has, unread
   } else {
     if (!find_rows(g, blockIdx.x, e, lo, cnt, m0)) return;
   }

@@ -422,6 +422,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void grouped_wgrad_kernel(GroupedArg
   const int m0 = 256 * (in / nt), n0 = BN * (in % nt);
   int lo, cnt;
   expert_rows(g.offsets, e, g.M, lo, cnt);
+  if (g.accumulate && cnt == 0) return;  // dw keeps what it has, unread
   tile_by_rows<G_TN>(g, smem, e, lo, cnt, m0, n0, g.K - m0);
 }
 

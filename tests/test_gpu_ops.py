@@ -145,6 +145,20 @@ def test_grouped_wgrad_long_expert(rows):
     close(dw, want, ref.sum_bound(want, mag, rows, F32))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_grouped_wgrad_empty_experts_keep_dw(dtype):
+    """accumulate: an expert without rows keeps dw bit for bit (-0 and NaN payloads too)."""
+    g, counts, K, N = gen(5), [0, 70, 0, 3, 0], 72, 136
+    M = sum(counts)
+    a, d = normal(g, M, K, dtype=dtype), normal(g, M, N, dtype=dtype)
+    dw = torch.full((5, K, N), -0.0, device="cuda")
+    dw[:, 3] = torch.tensor([0x7FA12345], dtype=torch.int32, device="cuda").view(F32)
+    start = dw.clone()
+    moe.moe_grouped_wgrad(a, d, ref.offsets_of(counts), dw, accumulate=True)
+    for e, c in enumerate(counts):
+        assert torch.equal(dw[e].view(torch.int32), start[e].view(torch.int32)) == (c == 0), e
+
+
 def test_grouped_no_rows():
     off = torch.zeros(4, dtype=torch.int32, device="cuda")
     a, w = torch.empty(0, 64, device="cuda", dtype=BF), torch.full((3, 64, 64), NAN, device="cuda", dtype=BF)
