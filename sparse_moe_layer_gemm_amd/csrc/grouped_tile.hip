@@ -31,11 +31,10 @@
 // one large matrix runs at 1.36. Without its loads it takes 1.16 ms, without its
 // MFMAs 1.12, without both 0.53, the MFMAs alone 0.94: no single part bounds it,
 // what remains is how far they overlap between barriers. The weight gradient
-// 64 x 5120 x 1536 over 32768 rows takes 0.84-0.88 ms, its 2 GB of fp32 results and
+// 64 x 5120 x 1536 over 32768 rows takes 0.75 ms, its 2 GB of fp32 results and
 // the short sums (16 steps a tile) weighing most. Two workgroups of 256 x 128 per
 // CU were 20% slower, four wavefronts of 128 x 128 spill, and one workgroup per CU
-// that loads the next tile during its epilogue was 10-15% slower (3% faster for
-// the weight gradient): dropped.
+// that loads the next tile during its epilogue was 10-15% slower: dropped.
 // The MFMA takes the column operand first, so that a lane ends with four
 // adjacent columns of a row and the epilogue packs them without shuffles.
 #include "grouped_common.h"
@@ -105,7 +104,9 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, uint8_t* smem, i
   constexpr int NSA = LAY == G_TN ? 3 : 2, NSB = 5 - NSA, B0 = NSA * PAIR;
   // 1 KB loads per wavefront and pair: 8 rows of 128 bytes, or 2 depth rows of 512
   constexpr int LA = A_ROWS ? MT / 2 : 4, LB = 4;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  // fresh: the weight gradient's loop over tiles keeps none of what follows in registers
+  const int tid = LAY == G_TN ? (int)fresh(threadIdx.x) : (int)threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int wm = wave / WN, wn = wave % WN;
   const int depth = LAY == G_TN ? cnt : g.K;
   const int np = (depth + 63) >> 6;
@@ -412,18 +413,66 @@ __global__ __launch_bounds__(64 * WAVES, 1) void grouped_tile_kernel(GroupedArgs
   tile_by_rows<LAY>(g, smem, t.e, t.lo, t.cnt, t.m0, BN * t.nt, t.cnt - t.m0);
 }
 
-// Weight gradient: mt x nt tiles per expert, all known in advance.
+// Weight gradient: mt x nt tiles per expert. Each XCD takes a run of them in expert
+// order (an expert's tiles share their lines of a and d in its L2) that costs an
+// eighth of the whole; its 32 workgroups, one per CU, take them in turn. A tile
+// costs its rows, and what kTileRows rows cost for its start and results (more
+// with accumulate, which reads dw; 256 to 512 and 512 to 1024 are within 6%).
+// Equal numbers of tiles per XCD instead: 835 against 750 us for 64 x 5120 x 1536
+// over 32768 uneven rows, 1990 against 890 for Zipf loads in order (748 against
+// 762 for even ones); a workgroup per tile: 766.
+constexpr int kTileRows = 384, kTileRowsAcc = 768, kGrid = 256;
 __global__ __launch_bounds__(64 * WAVES, 1) void grouped_wgrad_kernel(GroupedArgs g, int mt, int nt) {
   __shared__ __align__(1024) uint8_t smem[LDS_BYTES];
-  const int total = g.E * mt * nt, per = (total + 7) >> 3, slot = blockIdx.x >> 3;
-  const int item = (blockIdx.x & 7) * per + slot;
-  if (slot >= per || item >= total) return;
-  const int e = item / (mt * nt), in = item - e * (mt * nt);
-  const int m0 = 256 * (in / nt), n0 = BN * (in % nt);
-  int lo, cnt;
-  expert_rows(g.offsets, e, g.M, lo, cnt);
-  if (g.accumulate && cnt == 0) return;  // dw keeps what it has, unread
-  tile_by_rows<G_TN>(g, smem, e, lo, cnt, m0, n0, g.K - m0);
+  const int lane = threadIdx.x & 63, tiles = mt * nt;
+  uint32_t cost[4], mine = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = 4 * lane + i;
+    cost[i] = 0;
+    if (e < g.E) {
+      int lo, cnt;
+      expert_rows(g.offsets, e, g.M, lo, cnt);
+      if (cnt > 0 || !g.accumulate) cost[i] = (uint32_t)(cnt + (g.accumulate ? kTileRowsAcc : kTileRows)) >> 4;
+    }
+    mine += cost[i];
+  }
+  uint32_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t v = __shfl_up(incl, d);
+    if (lane >= d) incl += v;
+  }
+  const uint32_t all = __builtin_amdgcn_readlane(incl, 63);
+  if (all == 0) return;
+  // first tile whose start lies at or behind x eighths of the cost
+  auto border = [&](uint32_t x) -> int {
+    const uint32_t at = x * all;  // in eighths
+    if (x == 8) return g.E * tiles;
+    if (x == 0) return 0;
+    const int src = __builtin_ctzll(__ballot(8 * incl >= at));
+    uint32_t base = incl - mine, c = cost[0];
+    int e = 4 * lane;
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      if (at > 8 * (base + c)) {
+        base += c;
+        c = cost[i], e = 4 * lane + i;
+      }
+    const uint32_t into = __builtin_amdgcn_readlane(at - 8 * base, src), w = 8 * __builtin_amdgcn_readlane(c, src);
+    const int t = (int)ceilf((float)into * (float)tiles / (float)w);
+    return min(__builtin_amdgcn_readlane(e, src) * tiles + min(max(t, 0), tiles), g.E * tiles);
+  };
+  const int first = border(blockIdx.x & 7), last = border((blockIdx.x & 7) + 1);
+  for (int item = first + (int)(blockIdx.x >> 3); item < last; item += gridDim.x >> 3) {
+    const int e = item / tiles, in = item - e * tiles;
+    const int m0 = 256 * (in / nt), n0 = BN * (in % nt);
+    int lo, cnt;
+    expert_rows(g.offsets, e, g.M, lo, cnt);
+    if (g.accumulate && cnt == 0) continue;  // dw keeps what it has, unread
+    tile_by_rows<G_TN>(g, smem, e, lo, cnt, m0, n0, g.K - m0);
+    __syncthreads();
+  }
 }
 
 }  // namespace
@@ -433,8 +482,8 @@ hipError_t launch_grouped_tile(GroupedLayout lay, const GroupedArgs& a, hipStrea
   if (lay == G_TN) {
     const int mt = (a.K + 255) / 256;
     const long long n = ((long long)a.E * mt * nt + 7) / 8 * 8;
-    if (n * lanes >= (1LL << 32)) return hipErrorInvalidValue;
-    grouped_wgrad_kernel<<<(unsigned)n, lanes, 0, st>>>(a, mt, nt);
+    if (n >= (1LL << 30)) return hipErrorInvalidValue;  // tiles are counted in 32 bits
+    grouped_wgrad_kernel<<<(unsigned)(n < kGrid ? n : kGrid), lanes, 0, st>>>(a, mt, nt);
     return hipGetLastError();
   }
   const long long n = tile_grid(a, 256, nt);
