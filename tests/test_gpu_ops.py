@@ -145,6 +145,37 @@ def test_grouped_wgrad_long_expert(rows):
     close(dw, want, ref.sum_bound(want, mag, rows, F32))
 
 
+SKEWED = {
+    "falling": [1200 // (e + 1) for e in range(256)],
+    "rising": [1200 // (256 - e) for e in range(256)],
+    "one": [0] * 131 + [2000] + [0] * 124,
+    "ends": [700] + [0] * 254 + [900],
+    "one in eight": [300 if e % 8 == 7 else 0 for e in range(96)],
+    "even": [64] * 256,
+    "empty": [0] * 200,
+    "few": [5, 0, 4000],
+}
+
+
+@pytest.mark.parametrize("acc", [False, True])
+@pytest.mark.parametrize("load", SKEWED)
+def test_grouped_wgrad_skewed_loads(load, acc):
+    """More tiles than workgroups, shared out by uneven costs: every tile is written once."""
+    g, counts = gen(11), SKEWED[load]
+    K, N, M = 264, 520, sum(counts)
+    if len(counts) < 64:
+        K, N = 2056, 2568
+    a, d = normal(g, M, K), normal(g, M, N)
+    start = normal(g, len(counts), K, N, dtype=F32) if acc else torch.full((len(counts), K, N), NAN, device="cuda")
+    dw, big = ref.guarded(start, 16, 7.0)
+    moe.moe_grouped_wgrad(a, d, ref.offsets_of(counts), dw, accumulate=acc)
+    want, mag = ref.wgrad64(a.double(), d, counts)
+    if acc:
+        want, mag = want + start.double(), mag + start.double().abs()
+    close(dw, want, ref.sum_bound(want, mag, max(counts) + 1, F32))
+    assert ref.guards_intact(big, 16, 7.0)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_grouped_wgrad_empty_experts_keep_dw(dtype):
     """accumulate: an expert without rows keeps dw bit for bit (-0 and NaN payloads too)."""
