@@ -176,6 +176,21 @@ def test_grouped_wgrad_skewed_loads(load, acc):
     assert ref.guards_intact(big, 16, 7.0)
 
 
+@pytest.mark.parametrize("load", ["rising", "one in eight", "few"])
+def test_grouped_wgrad_skewed_gathered_bf16(load):
+    """The same with gathered rows (an index twice and bad ones) and bf16 results, rows behind the last expert."""
+    rng, g, counts = random.Random(3), gen(12), SKEWED[load]
+    K, N, used = (264, 520, sum(counts)) if len(counts) > 64 else (2056, 2568, sum(counts))
+    a, d = normal(g, 501, K), normal(g, used + 9, N)
+    d[used:] = NAN
+    idx = index_for(rng, used + 9, 501, 3, True)
+    dw, big = ref.guarded(torch.full((len(counts), K, N), NAN, device="cuda", dtype=BF), 16, 7.0)
+    moe.moe_grouped_wgrad(a, d, ref.offsets_of(counts), dw, row_index=idx, row_div=3)
+    want, mag = ref.wgrad64(ref.gather64(a, used, idx[:used], 3), d[:used], counts)
+    close(dw, want, ref.sum_bound(want, mag, max(counts) + 1, BF))
+    assert ref.guards_intact(big, 16, 7.0)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_grouped_wgrad_empty_experts_keep_dw(dtype):
     """accumulate: an expert without rows keeps dw bit for bit (-0 and NaN payloads too)."""
