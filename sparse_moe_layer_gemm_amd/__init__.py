@@ -319,10 +319,15 @@ def moe_forward_noalloc(x, w_router, bias, w: ExpertWeights, I: int, k: int, out
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() builds an object: 2.7 us a call
 _current_device = torch._C._cuda_getDevice
 _FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_I32_MAX = (1 << 31) - 1  # ctypes passes larger values on modulo 2^32, past the library's checks
 
 
 def _refuse(fn: str, what: str):
     raise ValueError(f"{fn}: {what}")
+
+
+def _too_wide(fn: str):
+    _refuse(fn, "every size but a number of rows must be below 2^31")
 
 
 def _float(t: torch.Tensor) -> int:
@@ -370,6 +375,8 @@ def _check_rows(fn, M, E, offsets, row_index, row_div):
             _refuse(fn, "row_index must be int32 [M]")
         if row_div < 1:
             _refuse(fn, "row_div must be positive")
+        if row_div > _I32_MAX:
+            _too_wide(fn)
 
 
 def moe_grouped_gemm(a, w, offsets, out, row_index=None, row_div: int = 1, w_trans: bool = False,
@@ -386,6 +393,8 @@ def moe_grouped_gemm(a, w, offsets, out, row_index=None, row_div: int = 1, w_tra
         _refuse(fn, "shapes of a, w and out do not match")
     if w.dtype is not a.dtype:
         _refuse(fn, "a and w must have one dtype")
+    if (K | N | E) > _I32_MAX:
+        _too_wide(fn)
     _check_rows(fn, M, E, offsets, row_index, row_div)
     t_in, t_out = _float(a), _float(out)
     dev, (pa, pw, po, pout, pi) = _arrays(fn, (a, w, offsets, out, row_index))
@@ -406,6 +415,8 @@ def moe_grouped_wgrad(a, d, offsets, dw, row_index=None, row_div: int = 1, accum
         _refuse(fn, "shapes of a, d and dw do not match")
     if a.dtype is not d.dtype:
         _refuse(fn, "a and d must have one dtype")
+    if (K | N | E) > _I32_MAX:
+        _too_wide(fn)
     _check_rows(fn, M, E, offsets, row_index, row_div)
     t_in, t_out = _float(a), _float(dw)
     dev, (pa, pd, po, pw, pi) = _arrays(fn, (a, d, offsets, dw, row_index))
@@ -421,6 +432,8 @@ def moe_swiglu(a, h, stream=None):
         _refuse(fn, "a must be [M, 2I] and h [M, I]")
     if a.dtype is not h.dtype:
         _refuse(fn, "a and h must have one dtype")
+    if sh[1] > _I32_MAX:
+        _too_wide(fn)
     t_in = _float(a)
     dev, (pa, ph) = _arrays(fn, (a, h))
     _run(fn, _lib.moe_swiglu, dev, stream, pa, t_in, sh[0], sh[1], ph)
@@ -437,6 +450,8 @@ def moe_swiglu_backward(a, dh, da, h=None, stream=None):
         _refuse(fn, "da is shaped as a, h as dh")
     if dh.dtype is not t or da.dtype is not t or (h is not None and h.dtype is not t):
         _refuse(fn, "all tensors must have one dtype")
+    if sh[1] > _I32_MAX:
+        _too_wide(fn)
     t_in = _float(a)
     dev, (pa, pdh, pda, ph) = _arrays(fn, (a, dh, da, h))
     _run(fn, _lib.moe_swiglu_backward, dev, stream, pa, pdh, t_in, sh[0], sh[1], pda, ph)
@@ -450,6 +465,8 @@ def moe_finalize_backward(dout, y_sorted, pair_pos, topk_w, dy_sorted, dtopk_w, 
     if len(sd) != 2 or len(sw) != 2 or sw[0] != sd[0] or topk_w.dtype is not torch.float32:
         _refuse(fn, "dout must be [T, H] and topk_w fp32 [T, k]")
     (T, H), k = sd, sw[1]
+    if (H | k) > _I32_MAX:
+        _too_wide(fn)
     if pair_pos.dtype is not torch.int32 or pair_pos.numel() != T * k:
         _refuse(fn, "pair_pos must be int32 [T*k]")
     if y_sorted is not None and (y_sorted.dtype is not torch.float32 or y_sorted.shape != (T * k, H)):
@@ -466,6 +483,8 @@ def moe_finalize_backward(dout, y_sorted, pair_pos, topk_w, dy_sorted, dtopk_w, 
 
 def moe_mxfp4_scale_stride(K: int) -> int:
     """Scale bytes per row of K MXFP4 values: K / 32 rounded up to a multiple of 4."""
+    if abs(K) > _I32_MAX:
+        _too_wide("moe_mxfp4_scale_stride")
     return _lib.moe_mxfp4_scale_stride(K)
 
 
@@ -489,6 +508,8 @@ def moe_mxfp4_quantize(x, codes, scales, trans: bool = False, stream=None):
         _check_mx(fn, codes, scales, (B, C) if trans else (B, R), R if trans else C)
     else:
         _refuse(fn, "x must have two or three dimensions")
+    if C > _I32_MAX:
+        _too_wide(fn)
     t_in = _float(x)
     dev, (px, pc, ps) = _arrays(fn, (x, codes, scales))
     _run(fn, _lib.moe_mxfp4_quantize, dev, stream, px, t_in, 1 if trans else 0, B, R, C, pc, ps)
@@ -502,6 +523,8 @@ def moe_mxfp4_dequantize(codes, scales, out, stream=None):
         _refuse(fn, "out must be [..., K]")
     K = so[-1]
     _check_mx(fn, codes, scales, so[:-1], K)
+    if K > _I32_MAX:
+        _too_wide(fn)
     t_out = _float(out)
     dev, (pc, ps, po) = _arrays(fn, (codes, scales, out))
     _run(fn, _lib.moe_mxfp4_dequantize, dev, stream, pc, ps, out.numel() // max(K, 1), K, t_out, po)
@@ -516,6 +539,8 @@ def moe_mxfp4_grouped_gemm(a_codes, a_scales, w_codes, w_scales, offsets, out, r
     if len(sa) != 2 or len(sw) != 3 or len(so) != 2:
         _refuse(fn, "a_codes and out are matrices, w_codes [E, N, K/2]")
     (rows, half), (M, N), E = sa, so, sw[0]
+    if (2 * half | N | E) > _I32_MAX:
+        _too_wide(fn)
     _check_mx(fn, a_codes, a_scales, (rows,), 2 * half)
     _check_mx(fn, w_codes, w_scales, (E, N), 2 * half)
     _check_rows(fn, M, E, offsets, row_index, row_div)
