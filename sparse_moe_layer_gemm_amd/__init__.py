@@ -141,6 +141,19 @@ def _check(fn: str, status: int):
         raise MoEError(fn, status)
 
 
+_I32_MAX = (1 << 31) - 1  # ctypes passes larger values on modulo 2^32, past the library's checks
+
+
+def _too_wide(fn: str):
+    raise ValueError(f"{fn}: every size but a number of rows must be below 2^31")
+
+
+def _int32s(fn: str, *values):
+    for v in values:
+        if abs(v) > _I32_MAX:
+            _too_wide(fn)
+
+
 @dataclasses.dataclass
 class ExpertWeights:
     """Device expert weights of one layer (layouts in include/moe.h)."""
@@ -161,6 +174,7 @@ class ExpertWeights:
 
 # ---------------------------------------------------------------- the C ABI, same names
 def moe_route_workspace_size(T: int, H: int, E: int) -> int:
+    _int32s("moe_route_workspace_size", H, E)
     return _lib.moe_route_workspace_size(T, H, E)
 
 
@@ -168,6 +182,7 @@ def moe_route(x, w_router, bias, k: int, logits_dtype: int, logits, logits_f32, 
               workspace, stream=None):
     T, H = x.shape
     E = w_router.shape[1]
+    _int32s("moe_route", H, E, k)
     _check("moe_route", _lib.moe_route(
         _ptr(x), _dt(x), T, H, _ptr(w_router), _ptr(bias), E, k, logits_dtype, _ptr(logits),
         _ptr(logits_f32), _ptr(topk_ids), _ptr(topk_w), _ptr(workspace),
@@ -175,12 +190,14 @@ def moe_route(x, w_router, bias, k: int, logits_dtype: int, logits, logits_f32, 
 
 
 def moe_permute_workspace_size(T: int, k: int, E: int) -> int:
+    _int32s("moe_permute_workspace_size", k, E)
     return _lib.moe_permute_workspace_size(T, k, E)
 
 
 def moe_permute(topk_ids, E: int, counts, offsets, sorted_pair, pair_pos, workspace=None,
                 stream=None):
     T, k = topk_ids.shape
+    _int32s("moe_permute", k, E)
     if workspace is None:
         need = moe_permute_workspace_size(T, k, E)
         workspace = globals()["workspace"](need, topk_ids.device) if need else None
@@ -191,6 +208,7 @@ def moe_permute(topk_ids, E: int, counts, offsets, sorted_pair, pair_pos, worksp
 
 
 def moe_experts_workspace_size(T: int, H: int, I: int, E: int, k: int, w: ExpertWeights) -> int:
+    _int32s("moe_experts_workspace_size", H, I, E, k)
     s = w.c_struct()
     return _lib.moe_experts_workspace_size(T, H, I, E, k, ctypes.byref(s))
 
@@ -198,6 +216,7 @@ def moe_experts_workspace_size(T: int, H: int, I: int, E: int, k: int, w: Expert
 def moe_experts(x, I: int, E: int, k: int, offsets, sorted_pair, w: ExpertWeights, y_sorted,
                 workspace, stream=None):
     T, H = x.shape
+    _int32s("moe_experts", H, I, E, k)
     s = w.c_struct()
     _check("moe_experts", _lib.moe_experts(
         _ptr(x), _dt(x), T, H, I, E, k, _ptr(offsets), _ptr(sorted_pair), ctypes.byref(s),
@@ -209,6 +228,7 @@ def moe_experts_rows16(x, I: int, E: int, k: int, offsets, sorted_pair, w: Exper
                        y16_scale, workspace, stream=None):
     """y16 [T*k, H] int16/uint16 (fp16 bits), y16_scale [T*k, H/64] uint8."""
     T, H = x.shape
+    _int32s("moe_experts_rows16", H, I, E, k)
     s = w.c_struct()
     _check("moe_experts_rows16", _lib.moe_experts_rows16(
         _ptr(x), _dt(x), T, H, I, E, k, _ptr(offsets), _ptr(sorted_pair), ctypes.byref(s),
@@ -219,6 +239,7 @@ def moe_experts_rows16(x, I: int, E: int, k: int, offsets, sorted_pair, w: Exper
 def moe_finalize_rows16(y16, y16_scale, pair_pos, topk_w, out, out_f32=None, stream=None):
     T, k = topk_w.shape
     H = y16.shape[1]
+    _int32s("moe_finalize_rows16", k, H)
     _check("moe_finalize_rows16", _lib.moe_finalize_rows16(
         _ptr(y16), _ptr(y16_scale), _ptr(pair_pos), _ptr(topk_w), T, k, H, _dt(out), _ptr(out),
         _ptr(out_f32), _stream(stream)))
@@ -227,6 +248,7 @@ def moe_finalize_rows16(y16, y16_scale, pair_pos, topk_w, out, out_f32=None, str
 def moe_finalize(y_sorted, pair_pos, topk_w, out, out_f32=None, stream=None):
     T, k = topk_w.shape
     H = y_sorted.shape[1]
+    _int32s("moe_finalize", k, H)
     _check("moe_finalize", _lib.moe_finalize(
         _ptr(y_sorted), _ptr(pair_pos), _ptr(topk_w), T, k, H, _dt(out), _ptr(out), _ptr(out_f32),
         _stream(stream)))
@@ -241,6 +263,7 @@ def moe_finalize_norm(y_sorted, pair_pos, topk_w, residual, gamma_post, gamma_ne
     for t in (residual, gamma_post, gamma_next, residual_out, normed):
         if t.dtype != torch.bfloat16:
             raise ValueError("moe_finalize_norm takes bf16 residual, norm weights and outputs")
+    _int32s("moe_finalize_norm", k, H)
     _check("moe_finalize_norm", _lib.moe_finalize_norm(
         _ptr(y_sorted), _ptr(pair_pos), _ptr(topk_w), T, k, H, _ptr(residual), _ptr(gamma_post),
         _ptr(gamma_next), float(eps), _ptr(residual_out), _ptr(normed), _stream(stream)))
@@ -254,6 +277,7 @@ def moe_finalize_norm_rows16(y16, y16_scale, pair_pos, topk_w, residual, gamma_p
     for t in (residual, gamma_post, gamma_next, residual_out, normed):
         if t.dtype != torch.bfloat16:
             raise ValueError("moe_finalize_norm_rows16 takes bf16 residual, norm weights and outputs")
+    _int32s("moe_finalize_norm_rows16", k, H)
     _check("moe_finalize_norm_rows16", _lib.moe_finalize_norm_rows16(
         _ptr(y16), _ptr(y16_scale), _ptr(pair_pos), _ptr(topk_w), T, k, H, _ptr(residual),
         _ptr(gamma_post), _ptr(gamma_next), float(eps), _ptr(residual_out), _ptr(normed),
@@ -261,6 +285,7 @@ def moe_finalize_norm_rows16(y16, y16_scale, pair_pos, topk_w, residual, gamma_p
 
 
 def moe_forward_workspace_size(T: int, H: int, I: int, E: int, k: int, w: ExpertWeights) -> int:
+    _int32s("moe_forward_workspace_size", H, I, E, k)
     s = w.c_struct()
     return _lib.moe_forward_workspace_size(T, H, I, E, k, ctypes.byref(s))
 
@@ -272,6 +297,7 @@ def moe_forward(x, w_router, bias, w: ExpertWeights, I: int, k: int, out, worksp
     E = w_router.shape[1]
     if logits_dtype is None:
         logits_dtype = _dt(x)
+    _int32s("moe_forward", H, I, E, k)
     s = w.c_struct()
     _check("moe_forward", _lib.moe_forward(
         _ptr(x), _dt(x), T, H, I, E, k, _ptr(w_router), _ptr(bias), ctypes.byref(s), _dt(out),
@@ -288,6 +314,7 @@ def moe_forward_norm(x, w_router, bias, w: ExpertWeights, I: int, k: int, residu
     for t in (x, residual, gamma_post, gamma_next, residual_out, normed):
         if t.dtype != torch.bfloat16:
             raise ValueError("moe_forward_norm takes bf16 x, residual, norm weights and outputs")
+    _int32s("moe_forward_norm", H, I, E, k)
     s = w.c_struct()
     _check("moe_forward_norm", _lib.moe_forward_norm(
         _ptr(x), T, H, I, E, k, _ptr(w_router), _ptr(bias), ctypes.byref(s), _ptr(residual),
@@ -307,6 +334,7 @@ def moe_forward_noalloc(x, w_router, bias, w: ExpertWeights, I: int, k: int, out
     E = w_router.shape[1]
     if logits_dtype is None:
         logits_dtype = _dt(x)
+    _int32s("moe_forward_noalloc", H, I, E, k)
     s = w.c_struct()
     _check("moe_forward_noalloc", _lib.moe_forward_noalloc(
         _ptr(x), _dt(x), T, H, I, E, k, _ptr(w_router), _ptr(bias), ctypes.byref(s), _dt(out),
@@ -319,15 +347,10 @@ def moe_forward_noalloc(x, w_router, bias, w: ExpertWeights, I: int, k: int, out
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() builds an object: 2.7 us a call
 _current_device = torch._C._cuda_getDevice
 _FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
-_I32_MAX = (1 << 31) - 1  # ctypes passes larger values on modulo 2^32, past the library's checks
 
 
 def _refuse(fn: str, what: str):
     raise ValueError(f"{fn}: {what}")
-
-
-def _too_wide(fn: str):
-    _refuse(fn, "every size but a number of rows must be below 2^31")
 
 
 def _float(t: torch.Tensor) -> int:
@@ -483,8 +506,7 @@ def moe_finalize_backward(dout, y_sorted, pair_pos, topk_w, dy_sorted, dtopk_w, 
 
 def moe_mxfp4_scale_stride(K: int) -> int:
     """Scale bytes per row of K MXFP4 values: K / 32 rounded up to a multiple of 4."""
-    if abs(K) > _I32_MAX:
-        _too_wide("moe_mxfp4_scale_stride")
+    _int32s("moe_mxfp4_scale_stride", K)
     return _lib.moe_mxfp4_scale_stride(K)
 
 
