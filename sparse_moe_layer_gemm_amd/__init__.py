@@ -344,8 +344,10 @@ def moe_forward_noalloc(x, w_router, bias, w: ExpertWeights, I: int, k: int, out
 
 # ---------------------------------------------------------------- operators around the layer
 # A small call is bound by its host side, so these check in line and touch each tensor once.
-_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() builds an object: 2.7 us a call
-_current_device = torch._C._cuda_getDevice
+# current_stream() builds an object, 2.7 us a call; torch's private names do not, where it has them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", lambda: torch.cuda.current_device())
 _FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
