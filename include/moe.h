@@ -312,9 +312,10 @@ moe_status moe_forward_noalloc(const void* x, int32_t x_dtype, int64_t T, int32_
  * rounded once, to nearest even, for MOE_BF16 outputs. accumulate (0 or 1)
  * adds to dw and needs MOE_F32 outputs. Sizes: 1 <= E <= 256, K and N
  * multiples of 8 up to 2^20, 0 <= M < 2^29, 1 <= a_rows < 2^31, row_div >= 1,
- * and (M / 16 + E) * ceil(N / 64) < 2^24 - 64 (else MOE_ERR_UNSUPPORTED). M == 0:
- * moe_grouped_gemm does nothing, moe_grouped_wgrad writes zeros. Outputs must
- * not overlap inputs (MOE_ERR_INVALID_ARGUMENT). No workspace. */
+ * and for moe_grouped_gemm (M / 16 + min(E, M)) * ceil(N / 64) < 2^24 - 64 (else
+ * MOE_ERR_UNSUPPORTED). M == 0: moe_grouped_gemm does nothing, moe_grouped_wgrad
+ * writes zeros (nothing with accumulate). Outputs must not overlap inputs
+ * (MOE_ERR_INVALID_ARGUMENT). No workspace. */
 moe_status moe_grouped_gemm(const void* a, int32_t dtype, int64_t a_rows, const int32_t* row_index,
                             int32_t row_div, const void* w, int32_t w_trans, int64_t M, int32_t K,
                             int32_t N, int32_t E, const int32_t* offsets, int32_t out_dtype,
@@ -382,7 +383,7 @@ moe_status moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int
 /* moe_grouped_gemm with both operands in MXFP4, on the fp4 MFMA:
  *   out[r] = sum_k a[i(r), k] * w[e, :, k]
  * a_codes, a_scales: a_rows rows of K; w_codes [E, N, K/2], w_scales [E, N, S].
- * Rows, row_index, row_div, M and the output as moe_grouped_gemm; every product
+ * Rows, row_index, row_div, M, its limit and the output as moe_grouped_gemm; every product
  * exact, sums in fp32 (fixed order). K a multiple of 32, N of 8, a_scales below
  * 4095 MiB (else MOE_ERR_UNSUPPORTED). */
 moe_status moe_mxfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t a_rows,

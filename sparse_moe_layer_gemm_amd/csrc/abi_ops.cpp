@@ -13,7 +13,7 @@
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxSorted = int64_t(1) << 29;  // rows of a grouped product (grid size)
+constexpr int64_t kMaxSorted = int64_t(1) << 29;  // rows of a grouped product (row indices stay below 2^31)
 constexpr int32_t kMaxWidth = 1 << 20;            // K and N of a grouped product
 constexpr int64_t kMaxBytes = int64_t(1) << 46;  // no array is larger than the address space
 constexpr int64_t kMaxScales = 0xFFF00000ll;       // bytes of a's MXFP4 scales (32-bit buffer offsets)
@@ -45,7 +45,7 @@ moe_status check_grouped(int64_t a_rows, const int32_t* row_index, int32_t row_d
                          int32_t K, int32_t N, int32_t E, int32_t k_unit) {
   if (M < 0 || K <= 0 || N <= 0 || E <= 0 || a_rows < 0) return MOE_ERR_INVALID_ARGUMENT;
   if (E > 256 || K % k_unit != 0 || N % 8 != 0 || K > kMaxWidth || N > kMaxWidth ||
-      M >= kMaxSorted || a_rows > kMaxRows || !moe::grouped_fits(M, K, N, E))
+      M >= kMaxSorted || a_rows > kMaxRows)
     return MOE_ERR_UNSUPPORTED;
   if (row_index) {
     if (row_div < 1) return MOE_ERR_INVALID_ARGUMENT;
@@ -67,6 +67,7 @@ moe_status moe_grouped_gemm(const void* a, int32_t dtype, int64_t a_rows, const 
     return MOE_ERR_INVALID_ARGUMENT;
   moe_status s = check_grouped(a_rows, row_index, row_div, M, K, N, E, 8);
   if (s != MOE_OK) return s;
+  if (!moe::grouped_fits(M, N, E)) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
   if (a_rows < 1) return MOE_ERR_INVALID_ARGUMENT;
   if (!array_ok(a) || !array_ok(w) || !array_ok(offsets) || !array_ok(out) || !aligned16(row_index))
@@ -216,6 +217,7 @@ moe_status moe_mxfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scale
   if (!is_float(out_dtype)) return MOE_ERR_INVALID_ARGUMENT;
   moe_status s = check_grouped(a_rows, row_index, row_div, M, K, N, E, 32);
   if (s != MOE_OK) return s;
+  if (!moe::grouped_fits(M, N, E)) return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
   if (a_rows < 1) return MOE_ERR_INVALID_ARGUMENT;
   if (!array_ok(a_codes) || !array_ok(a_scales) || !array_ok(w_codes) || !array_ok(w_scales) ||

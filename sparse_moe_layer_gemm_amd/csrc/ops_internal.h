@@ -30,14 +30,13 @@ enum GroupedLayout {
 };
 enum GroupedInput { G_BF16 = 0, G_MX = 1 };
 
-// Whether every launch below stays within 2^31 work items and 2^32 lanes: the
+// Whether every launch of a product stays within 2^31 work items and 2^32 lanes: the
 // smallest row tile has 16 rows, the smallest column tile 64 columns, and a
-// workgroup of the streaming kernels up to 256 lanes (weight gradients: 64 x 64
-// tiles of 256 lanes).
-inline bool grouped_fits(long long M, int K, int N, int E) {
+// workgroup of the streaming kernels up to 256 lanes. Weight gradients need no such
+// limit: their grids go by dw's tiles (at most 256 * 2^14 of 64 rows, 2^14 of 64 columns).
+inline bool grouped_fits(long long M, int N, int E) {
   const long long cols = (N + 63) / 64, rows = M / 16 + (E < M ? E : M);
-  const long long wgrad = (long long)E * ((K + 63) / 64);
-  return rows * cols < (1 << 24) - 64 && wgrad < (1 << 24);
+  return rows * cols < (1 << 24) - 64;
 }
 
 // fp32 products and weight gradients (the fp32 layer's path).
