@@ -17,6 +17,7 @@ __global__ __launch_bounds__(1024) void finalize_backward_kernel(
     const void* __restrict__ dout, const float* __restrict__ y, const int32_t* __restrict__ pos,
     const float* __restrict__ w, int T, int k, int H, void* __restrict__ dy,
     float* __restrict__ dw) {
+  static_assert(DY_BF16 || !NT, "fp32 results go through the caches");
   __shared__ float part[16][SL];
   const int tid = threadIdx.x;
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(1024) void finalize_backward_kernel(
 #pragma unroll
               for (int i = 0; i < 4; ++i) o[i] = bf16_pair(wj[j] * d[2 * i], wj[j] * d[2 * i + 1]);
               store_once<NT>(reinterpret_cast<u32x4*>(static_cast<uint16_t*>(dy) + row[j] * H + c), o);
-            } else {
+            } else {  // through the caches, which join a lane's two halves of its 32 bytes
               f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(dy) + row[j] * H + c);
               q[0] = f32x4{wj[j] * d[0], wj[j] * d[1], wj[j] * d[2], wj[j] * d[3]};
               q[1] = f32x4{wj[j] * d[4], wj[j] * d[5], wj[j] * d[6], wj[j] * d[7]};
@@ -110,15 +111,17 @@ hipError_t launch_finalize_backward(const void* dout, bool dout_bf16, const floa
   // All slots together read dout once (T = 8192, k = 8, H = 5120: 399 us; 4 slots
   // 419, 2 slots 447); few tokens spread their slots over more workgroups.
   const int tb = T < kMaxBlocks ? T : kMaxBlocks;
-  const bool nt = (long long)T * k * H * (4 + (dy_bf16 ? 2 : 4)) > kStreamBytes;
+  // Large calls store bf16 results past the caches. Not fp32 ones (T = 8192, k = 8, H = 5120: 570 us through
+  // the caches, 713 past them), nor do the loads of y go past (bf16 results 416 and 426 us).
+  const bool nt = dy_bf16 && (long long)T * k * H * 6 > kStreamBytes;
 #define MOE_FIN_BWD(A, B, SL, NT)                                                            \
   finalize_backward_kernel<A, B, SL, NT><<<dim3(tb, (k + SL - 1) / SL), lanes, 0, st>>>(      \
       dout, y, pair_pos, w, T, k, H, dy, dw)
 #define MOE_FIN_BWD_BY_SIZE(A, B)            \
   if (T < 512)                               \
     MOE_FIN_BWD(A, B, 2, false);             \
-  else if (nt)                               \
-    MOE_FIN_BWD(A, B, 8, true);              \
+  else if (B && nt)                          \
+    MOE_FIN_BWD(A, B, 8, B);                 \
   else                                       \
     MOE_FIN_BWD(A, B, 8, false)
   if (dout_bf16) {
