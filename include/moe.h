@@ -333,8 +333,8 @@ moe_status moe_grouped_wgrad(const void* a, int32_t dtype, int64_t a_rows, const
  * in fp32, rounded once to dtype (MOE_BF16 or MOE_F32, of all arrays). The
  * backward call forms h again if h is not NULL, so that the forward pass need
  * not keep it. da may be a itself and h may be dh itself (in place);
- * any other overlap returns MOE_ERR_INVALID_ARGUMENT. I a multiple of 8,
- * 0 <= M < 2^31 (0: a no-op). */
+ * any other overlap returns MOE_ERR_INVALID_ARGUMENT. I a multiple of 8 up to
+ * 2^30, 0 <= M < 2^31 (0: a no-op), M * I at most 2^35 - 2^11. */
 moe_status moe_swiglu(const void* a, int32_t dtype, int64_t M, int32_t I, void* h, void* stream);
 moe_status moe_swiglu_backward(const void* a, const void* dh, int32_t dtype, int64_t M, int32_t I,
                                void* da, void* h, void* stream);
@@ -371,9 +371,12 @@ moe_status moe_finalize_backward(const void* dout, int32_t dout_dtype, const flo
  * x is dtype (MOE_BF16 or MOE_F32): with trans = 0 [B, R, C], quantised along
  * C into rows (B, R); with trans = 1 [B, R, C] quantised along R into rows
  * (B, C), which turns weights stored [E, K, N] into the [E, N, K] that
- * moe_mxfp4_grouped_gemm reads (C a multiple of 8).
+ * moe_mxfp4_grouped_gemm reads (C a multiple of 8). K up to 2^30, B and R below
+ * 2^31 (0: a no-op); B * R * C at most 2^35 - 2^11 with trans = 0, and
+ * B * ceil(K / 256) * ceil(C / 128) < 2^23 with trans = 1.
  * moe_mxfp4_dequantize writes the values of codes and scales, [R, K] dtype
- * (exact; both types hold every value a quantised block can have). */
+ * (exact; both types hold every value a quantised block can have); R * K at most
+ * 2^35 - 2^11. */
 int32_t moe_mxfp4_scale_stride(int32_t K);
 moe_status moe_mxfp4_quantize(const void* x, int32_t dtype, int32_t trans, int64_t B, int64_t R,
                               int32_t C, uint8_t* codes, uint8_t* scales, void* stream);

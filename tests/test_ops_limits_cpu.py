@@ -31,3 +31,28 @@ def test_weight_gradient_takes_any_rows(M, K, N, E, dt):
     ((1 << 28) - 321 * 16, 64, 256, INVAL), ((1 << 28) - 320 * 16, 64, 256, UNSUP), (1, 1 << 20, 256, INVAL)])
 def test_product_row_limit(M, N, E, want):
     assert gemm(M, 8, N, E) == want
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+@pytest.mark.parametrize("M,I,want", [((1 << 31) - 1, 8, INVAL), (1 << 31, 8, UNSUP), (1, 1 << 30, INVAL),
+                                      (1, (1 << 30) + 8, UNSUP), ((1 << 27) - 8, 256, INVAL), ((1 << 27) - 1, 256, UNSUP),
+                                      ((1 << 24) - 1, 2048, INVAL), (1 << 24, 2048, UNSUP)])
+def test_swiglu_limits(M, I, want, bwd):
+    """M * I up to 2^35 - 2^11."""
+    f = moe.load_library()
+    assert (f.moe_swiglu_backward(None, B, 1, M, I, C, None, None) if bwd else f.moe_swiglu(None, 1, M, I, B, None)) == want
+
+
+@pytest.mark.parametrize("trans,Bn,R,C,want", [
+    (0, 1, (1 << 24) - 1, 2048, INVAL), (0, 1, 1 << 24, 2048, UNSUP), (0, 4, 1 << 22, 2048, UNSUP),
+    (0, 1, 1, 1 << 30, INVAL), (0, 1, 1, (1 << 30) + 32, UNSUP),
+    # B * ceil(K / 256) * ceil(C / 128) below 2^23
+    (1, (1 << 23) - 1, 32, 8, INVAL), (1, 1 << 23, 32, 8, UNSUP), (1, 1 << 10, 256 * 128, 128 * 64, UNSUP),
+    (1, (1 << 10) - 1, 256 * 128, 128 * 64, INVAL), (1, 1, 1 << 30, 8, INVAL), (1, 1, (1 << 30) + 32, 8, UNSUP)])
+def test_quantise_limits(trans, Bn, R, C, want):
+    assert moe.load_library().moe_mxfp4_quantize(None, 1, trans, Bn, R, C, A, B, None) == want
+
+
+@pytest.mark.parametrize("R,K,want", [((1 << 24) - 1, 2048, INVAL), (1 << 24, 2048, UNSUP), (1, (1 << 31) - 32, INVAL)])
+def test_dequantise_limits(R, K, want):
+    assert moe.load_library().moe_mxfp4_dequantize(None, B, R, K, 1, C, None) == want
