@@ -4,8 +4,12 @@
 // A workgroup computes one 64 x 64 tile of one expert: 16-deep slices of both
 // operands go through LDS and four wavefronts of 32 x 32 feed the fp32 MFMA
 // 32x32x2. Every load checks its row, column and depth, so any size works.
-// Bound: the scalar loads and the barriers around each slice (0.07 PFLOP/s);
-// this path is for exactness, not for large products.
+// Bound: the scalar loads and the two barriers around each slice, which no MFMA
+// overlaps: 0.06 PFLOP/s, under half of the fp32 MFMA's rate (32768 rows x 5120 x 1536
+// over 64 experts 8.3 ms, the weight gradient 9.2 ms, 9.9 with accumulate, where every
+// value of dw is waited for by itself). One token through 8 of 256 experts takes 0.70
+// ms: 192 workgroups that walk 320 slices each. The path is as simple as it can be
+// and has not been tuned.
 #include "ops_common.h"
 
 namespace moe {

@@ -14,10 +14,11 @@
 // MFMA is 16x16x32 bf16, or the block-scaled 16x16x128 for MXFP4 (lane l: row
 // l % 16, block l / 16 of four).
 //
-// Measured at K = 5120, N = 1536: one token through 8 of 256 bf16 experts 25 us
-// (w [N, K] 22 us; 5 us without the weights, then 6.4 TB/s), 64 tokens 474 us (7.4
-// TB/s); MXFP4, 16 tokens, 71 us (6.0 TB/s; 94 us with 64-byte pieces and a load
-// per scale and step). The rings in flight, not their depth, set the rate: six or
+// Measured at K = 5120, N = 1536 with weights that no cache holds: one token through
+// 8 of 256 bf16 experts 31-32 us (w [N, K] 26 us; 24 and 21 us where the call before
+// it took the same experts; 5 us without the weights), 64 tokens through 180 of them
+// 475 us (6.0 TB/s); MXFP4, 16 tokens through 88 of 256, 71-76 us (4.9-5.2 TB/s; 94 us
+// with 64-byte pieces and a load per scale and step). The rings in flight, not their depth, set the rate: six or
 // eight wavefronts per CU with two to four stages are within 3%.
 #include "grouped_common.h"
 
@@ -285,17 +286,34 @@ hipError_t launch(const GroupedArgs& a, hipStream_t st) {
 }
 }  // namespace
 
-// The streaming kernel or the 256 x 256 tiles? Measured at K = 5120, N = 1536, us
-// (bf16 w [K, N] / MXFP4), streaming against tiles:
-//   64 experts (384 tiles), rows per expert 4: 177 / 50 against 178 / 70; 8: 188 / 59
-//     against 182 / 71; 16: 211 / 70 against 187 / 72; 32: 240 / 108 against 197 / 75
-//   24 experts (144 tiles), 8: 83 / 23 against 76 / 24; 32: 106 / 41 against 100 / 32
-//   8 experts (48 tiles), 16: 35 / 12 against 49 / 21; 64: 38 / 22 against 87 / 31
-//   1 expert (6 tiles), 64: 20 / 11 against 49 / 16
+// The streaming kernel or the 256 x 256 tiles? Measured at K = 5120, N = 1536 with
+// weights that no cache holds, us, streaming against tiles, for bf16 w [K, N], w [N, K]
+// and MXFP4 (an expert has 6 tiles per 256 rows, 24 streaming workgroups per 32):
+//   experts x rows   [K, N]      [N, K]      MXFP4
+//     1 x 64         20   46     15   45     10   20
+//     4 x 128        50   79     37   81     20   34
+//     8 x 16         33   62     28   69     11   30
+//     8 x 64         62   69     45   74     21   31
+//     8 x 128        78   84     58   88     31   34    tiles by the rule
+//    12 x 32         71   68     53   73     23   32
+//    16 x 32         75   70     57   75     24   32
+//    16 x 64         90   75     70   80     33   34    tiles by the rule
+//    20 x 32         79   75     62   80     26   34
+//    20 x 64        110   82     89   85     42   35    tiles by the rule
+//    24 x 8          79   74     76   79     25   34
+//    24 x 32        106  100      -    -     41   32    tiles by the rule (cached weights)
+//    64 x 8         191  184    169  186     52   72
+//    64 x 32        240  197      -    -    108   75    tiles by the rule (cached weights)
 // So: few rows per expert, where the weights bound both; or so few tiles that
-// they leave half of the 256 CUs idle, while the streaming workgroups (four to
-// a tile's columns, up to 32 rows each) still run side by side, two per CU. The
-// scales of MXFP4 columns have to fit in LDS.
+// they leave half of the 256 CUs idle, while there are at most two streaming
+// workgroups per CU (bf16: they run side by side; MXFP4 with 32 rows: two fit in a
+// CU's LDS up to K = 2560, at 5120 one does, and is faster than the tiles all the
+// same). Where it is off: 8 x 128 would stream 8, 52 and 13% sooner. It knows neither
+// the layout (at 8 rows and at 12 to 20 x 32 it costs w [K, N] 4-7% and saves
+// w [N, K] 4-27%) nor the loads, only their average: 2048 rows
+// of one of 256 experts take 133 / 120 / 60 us in 16-row streaming tiles, 110 / 97 / 37
+// in 256-row ones (1024 rows of one and one of each other: 715 / 686 / 206 against
+// 679 / 689 / 249). The scales of MXFP4 columns have to fit in LDS.
 bool prefer_stream(GroupedInput in, const GroupedArgs& a) {
   if (in == G_MX && scale_bytes(a.S, 2) > 40 * 1024) return false;
   const long long e = a.E < a.M ? a.E : a.M;
@@ -307,7 +325,8 @@ bool prefer_stream(GroupedInput in, const GroupedArgs& a) {
 hipError_t launch_grouped_stream(GroupedInput in, GroupedLayout lay, const GroupedArgs& a,
                                  hipStream_t st) {
   const bool wide = a.M > 16LL * a.E;  // more than 16 rows per expert on average
-  // wavefronts and stages so that two workgroups (MXFP4: three) share a CU's LDS
+  // wavefronts and stages so that two workgroups share a CU's LDS (MXFP4, whose scales
+  // grow with K: up to K = 7680 with 16 rows, 2560 with 32, then one)
   if (in == G_MX) return wide ? launch<S_MX, 2, 3, 2>(a, st) : launch<S_MX, 1, 3, 2>(a, st);
   if (lay == G_NN) return wide ? launch<S_NN, 2, 4, 3>(a, st) : launch<S_NN, 1, 4, 4>(a, st);
   return wide ? launch<S_NT, 2, 3, 2>(a, st) : launch<S_NT, 1, 4, 2>(a, st);

@@ -31,8 +31,10 @@
 // one large matrix runs at 1.36. Without its loads it takes 1.16 ms, without its
 // MFMAs 1.12, without both 0.53, the MFMAs alone 0.94: no single part bounds it,
 // what remains is how far they overlap between barriers. The weight gradient
-// 64 x 5120 x 1536 over 32768 rows takes 0.75 ms, its 2 GB of fp32 results and
-// the short sums (16 steps a tile) weighing most. Two workgroups of 256 x 128 per
+// 64 x 5120 x 1536 over 32768 rows takes 0.75-0.77 ms with fp32 results, 0.65 with bf16
+// ones. Its loads weigh most: a form that took 0.77 ms with bf16 results took 0.59
+// with nothing but them (40 GB/s per CU), 0.72 without its stores (four times the
+// rows: 2.65, 1.58 and 2.39 ms). Two workgroups of 256 x 128 per
 // CU were 20% slower, four wavefronts of 128 x 128 spill, and one workgroup per CU
 // that loads the next tile during its epilogue was 10-15% slower: dropped.
 // The MFMA takes the column operand first, so that a lane ends with four

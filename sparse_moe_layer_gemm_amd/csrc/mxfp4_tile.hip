@@ -14,8 +14,9 @@
 // K / 32 are cut off, never interpreted. Products of codes and scales are exact,
 // the sums fp32.
 //
-// Measured: 65536 rows x 5120 x 2560 over 64 uneven experts 0.53-0.54 ms (3.2
-// PFLOP/s, against 6.5 for the MFMA alone); at 0.56 ms it took 0.43 without its
+// Measured: 65536 rows x 5120 x 2560 over 64 uneven experts 0.53-0.56 ms by card
+// (3.1-3.2 PFLOP/s, against 6.5 for the MFMA alone; fp32 results 0.60); a form that
+// took 0.56 where this one takes 0.53 took 0.43 without its
 // loads and 0.47 without its MFMAs: the loads (40 GB/s per CU, bound by the latency of w's lines over two
 // stages) and 9 us of start and end per tile bound it. 64-byte rows in four stages
 // took 0.59, four wavefronts of 128 x 128 0.76, two workgroups of 256 x 128 per CU
