@@ -395,6 +395,49 @@ moe_status moe_mxfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scale
                                   int32_t K, int32_t N, int32_t E, const int32_t* offsets,
                                   int32_t out_dtype, void* out, void* stream);
 
+/* ------------------------------------------------------------ routing by scores
+ * The choice of experts for routers other than moe_route's, from logits [T, E]
+ * (dtype MOE_F32 or MOE_BF16; moe_route writes such logits). Per token:
+ *   scores   s = softmax of the logits over all E, or 1 / (1 + e^-logit) each
+ *   choices  c = s + bias (bias f32 [E], the balance of loads: it moves the choice,
+ *            not the weights); NULL: c = s, compared through the logits
+ *   groups   the experts in `groups` runs of E / groups; a group counts as its
+ *            largest choice (group_top 1) or the sum of its two largest (2; the one it
+ *            has, where there is no second); the group_k groups that count most stay
+ *   ids      the k largest choices of the groups that stay, in falling order
+ *   weights  w_j = scale * s[id_j], with renorm (1) divided by the sum of the chosen
+ *            scores (a sum of zero leaves zeros)
+ * Equal groups and equal choices go to the lowest index. Scores and choices are
+ * formed in fp64 and choices with a bias compared to 44 bits; the weights are
+ * rounded once. An expert whose logit is NaN or -infinity is left out: its score is
+ * 0, it is never chosen. Nor is one whose bias is NaN or -infinity. Slots for which
+ * no expert is left get id -1 and weight 0: moe_permute leaves such pairs without a
+ * row and the finalize calls add nothing for them. A logit of +infinity is the limit
+ * of large ones (several share the softmax evenly).
+ *   topk_ids [T, k] int32; topk_w [T, k] f32; scores [T, E] f32, or NULL
+ * 1 <= k <= 8, k <= E <= 256, groups (1: none) divides E, is at most 64 and
+ * 1 <= group_k <= groups with k <= group_k * E / groups; scale finite;
+ * 0 <= T < 2^24 (0: a no-op). Outputs overlap neither inputs nor each other.
+ * moe_select_backward, the gradient of the logits from those of the weights
+ * (dtopk_w [T, k]) and, unless NULL, of the scores (dscores f32 [T, E], for a loss
+ * on the loads), with the choice held fixed:
+ *   renorm: ds_j = scale / S (dw_j - sum_i dw_i s_i / S), S the sum of the chosen s
+ *   else:   ds_j = scale dw_j
+ *   g = dscores + ds at the ids
+ *   softmax: dl = s (g - sum_e s g);  sigmoid: dl = s (1 - s) g
+ * rounded once to dl_dtype (dlogits [T, E]). A slot whose id lies outside [0, E)
+ * has no gradient, nor has an expert that is left out; an expert that two slots
+ * name gets the sum. Limits as above. */
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+moe_status moe_select(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k,
+                      int32_t score, const float* bias, int32_t groups, int32_t group_k,
+                      int32_t group_top, int32_t renorm, float scale, int32_t* topk_ids,
+                      float* topk_w, float* scores, void* stream);
+moe_status moe_select_backward(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k,
+                               int32_t score, int32_t renorm, float scale, const int32_t* topk_ids,
+                               const float* dtopk_w, const float* dscores, int32_t dl_dtype,
+                               void* dlogits, void* stream);
+
 /* ------------------------------------------------------------ measurement
  * Not a step of the layer: the HBM read ceiling its bandwidth-bound kernels
  * are quoted against. Reads `bytes` (a multiple of 16) of device memory at buf

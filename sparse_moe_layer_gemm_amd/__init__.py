@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe.so")
 
 MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_FP4_E2M1 = 0, 1, 2, 3
 MOE_QMODE_W, MOE_QMODE_F8 = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 DTYPE_NAMES = {"f32": MOE_F32, "bf16": MOE_BF16, "fp8": MOE_FP8_E4M3, "fp4": MOE_FP4_E2M1}
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARGUMENT", 2: "MOE_ERR_UNSUPPORTED",
           3: "MOE_ERR_WORKSPACE_TOO_SMALL", 4: "MOE_ERR_LAUNCH"}
@@ -31,7 +32,8 @@ ENTRY_POINTS = ("moe_status_string", "moe_route_workspace_size", "moe_route",
                 "moe_forward", "moe_forward_norm", "moe_forward_noalloc",
                 "moe_hbm_read", "moe_grouped_gemm", "moe_grouped_wgrad", "moe_swiglu",
                 "moe_swiglu_backward", "moe_finalize_backward", "moe_mxfp4_scale_stride",
-                "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_grouped_gemm")
+                "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_grouped_gemm", "moe_select",
+                "moe_select_backward")
 
 
 class MoEError(RuntimeError):
@@ -102,6 +104,10 @@ def load_library(path: str = LIB_PATH):
         "moe_mxfp4_dequantize": (_i32, [_vp, _vp, _i64, _i32, _i32, _vp, _vp]),
         "moe_mxfp4_grouped_gemm": (_i32, [_vp, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _i32, _i32,
                                           _i32, _vp, _i32, _vp, _vp]),
+        "moe_select": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32,
+                              ctypes.c_float, _vp, _vp, _vp, _vp]),
+        "moe_select_backward": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _i32, ctypes.c_float, _vp,
+                                       _vp, _vp, _i32, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -349,6 +355,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", lambda: torch.cuda.current_device())
 _FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 
 
 def _refuse(fn: str, what: str):
@@ -573,6 +580,57 @@ def moe_mxfp4_grouped_gemm(a_codes, a_scales, w_codes, w_scales, offsets, out, r
         fn, (a_codes, a_scales, w_codes, w_scales, offsets, out, row_index))
     _run(fn, _lib.moe_mxfp4_grouped_gemm, dev, stream, pa, psa, rows, pi, row_div, pw, psw, M,
          2 * half, N, E, po, t_out, pout)
+
+
+def _check_select(fn, logits, topk_ids, per_slot, score):
+    """(T, E, k, score) of a routing call; per_slot: the fp32 [T, k] beside the ids."""
+    sl, si = logits.shape, topk_ids.shape
+    if len(sl) != 2 or len(si) != 2 or si[0] != sl[0]:
+        _refuse(fn, "logits must be [T, E] and topk_ids [T, k]")
+    if topk_ids.dtype is not torch.int32 or per_slot.dtype is not torch.float32 or per_slot.shape != si:
+        _refuse(fn, "topk_ids must be int32 and the weights (or their gradient) fp32, [T, k]")
+    if (sl[1] | si[1]) > _I32_MAX:
+        _too_wide(fn)
+    kind = _SCORES.get(score)
+    if kind is None:
+        _refuse(fn, "score must be 'softmax' or 'sigmoid'")
+    return sl[0], sl[1], si[1], kind
+
+
+def moe_select(logits, topk_ids, topk_w, score="softmax", bias=None, groups: int = 1, group_k: int = 1,
+               group_top: int = 1, renorm: bool = True, scale: float = 1.0, scores=None, stream=None):
+    """The k experts of each token by scores of logits [T, E] (bf16 or fp32) and their weights:
+    topk_ids int32 [T, k] (-1: no expert left), topk_w fp32 [T, k]. score: "softmax" or "sigmoid";
+    bias: fp32 [E], added to the scores for the choice; groups: the experts come from the group_k of
+    that many groups whose group_top (1 or 2) largest choices sum highest; renorm: weights divided
+    by their sum; scores: fp32 [T, E], receives all scores."""
+    fn = "moe_select"
+    T, E, k, kind = _check_select(fn, logits, topk_ids, topk_w, score)
+    if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (E,)):
+        _refuse(fn, "bias must be fp32 [E]")
+    if scores is not None and (scores.dtype is not torch.float32 or scores.shape != (T, E)):
+        _refuse(fn, "scores must be fp32 [T, E]")
+    _int32s(fn, groups, group_k, group_top)
+    t_in = _float(logits)
+    dev, (pl, pi, pw, pb, ps) = _arrays(fn, (logits, topk_ids, topk_w, bias, scores))
+    _run(fn, _lib.moe_select, dev, stream, pl, t_in, T, E, k, kind, pb, groups, group_k, group_top,
+         1 if renorm else 0, scale, pi, pw, ps)
+
+
+def moe_select_backward(logits, topk_ids, dtopk_w, dlogits, score="softmax", renorm: bool = True,
+                        scale: float = 1.0, dscores=None, stream=None):
+    """dlogits [T, E] (bf16 or fp32) of moe_select's weights for dtopk_w fp32 [T, k] and, if given,
+    of its scores for dscores fp32 [T, E]; the choice (topk_ids) is held fixed."""
+    fn = "moe_select_backward"
+    T, E, k, kind = _check_select(fn, logits, topk_ids, dtopk_w, score)
+    if dlogits.shape != (T, E):
+        _refuse(fn, "dlogits must be [T, E]")
+    if dscores is not None and (dscores.dtype is not torch.float32 or dscores.shape != (T, E)):
+        _refuse(fn, "dscores must be fp32 [T, E]")
+    t_in, t_out = _float(logits), _float(dlogits)
+    dev, (pl, pi, pw, ps, pd) = _arrays(fn, (logits, topk_ids, dtopk_w, dscores, dlogits))
+    _run(fn, _lib.moe_select_backward, dev, stream, pl, t_in, T, E, k, kind, 1 if renorm else 0,
+         scale, pi, pw, ps, t_out, pd)
 
 
 # ---------------------------------------------------------------- device plumbing

@@ -1,8 +1,6 @@
-// Device pieces of the tiled grouped products: compile-time loops, LDS fills
-// and fragment reads, and the map from a workgroup to an expert's tile.
+// Device pieces of the tiled grouped products: LDS fills and fragment reads, and
+// the map from a workgroup to an expert's tile.
 #pragma once
-
-#include <utility>
 
 #include "ops_common.h"
 
@@ -11,16 +9,6 @@ namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
-
-template <class F, int... I>
-__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-// f(0) .. f(N - 1) with the index as a compile-time constant
-template <int N, class F>
-__device__ __forceinline__ void static_for(F&& f) {
-  static_for_impl(f, std::make_integer_sequence<int, N>{});
-}
 
 // What loads of rows, columns or depths outside an operand read.
 __device__ const uint4 kZeros[4] = {};

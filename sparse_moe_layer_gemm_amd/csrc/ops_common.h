@@ -1,6 +1,8 @@
-// Device pieces of the operators around the layer: NaN-keeping bf16 rounding,
+// Device pieces of the operators around the layer: compile-time loops, NaN-keeping bf16 rounding,
 // wavefront reductions and the map from a work item to an expert's rows.
 #pragma once
+
+#include <utility>
 
 #include "device_common.h"
 #include "ops_internal.h"
@@ -10,6 +12,16 @@ namespace {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+template <class F, int... I>
+__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+// f(0) .. f(N - 1) with the index as a compile-time constant
+template <int N, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
 
 // fp32 -> bf16, nearest even (hardware conversion: NaN stays NaN, overflow
 // goes to infinity)

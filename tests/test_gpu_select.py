@@ -1,0 +1,233 @@
+"""Routing by scores and its gradient on the GPU against plain 64-bit forms."""
+import pytest
+import torch
+
+import sparse_moe_layer_gemm_amd as moe
+from tests import ops_ref, select_ref as ref
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+NAN, INF = float("nan"), float("inf")
+U = 2.0 ** -24
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def rows(T, E, dtype, seed):
+    """Random logits; from row 8 on (where there are so many) rows that are special."""
+    l = torch.randn(T, E, generator=gen(seed), device="cuda") * 2
+    special = [
+        lambda r: r.fill_(-INF), lambda r: r.fill_(0.25), lambda r: r.fill_(NAN), lambda r: r[: E - 1].fill_(-INF),
+        lambda r: r[::2].fill_(NAN), lambda r: r[E // 2:].fill_(INF), lambda r: r.mul_(1e37), lambda r: r.mul_(1e-38),
+        lambda r: r.sub_(400.0), lambda r: r.add_(60.0), lambda r: r[1:].fill_(-3e38), lambda r: r.copy_(r.sign() * 0.0),
+        lambda r: r[: E // 2].fill_(-INF), lambda r: r.sub_(2000.0), lambda r: r[0].fill_(INF),
+    ]
+    for i, f in enumerate(special):
+        if 8 + i < T:
+            f(l[8 + i])
+    return l.to(dtype)
+
+
+def run(l, k, spare=True, **kw):
+    """ids, weights and scores of a call, all between guards."""
+    T, E = l.shape
+    ids, ib = ops_ref.guarded(torch.full((T, k), -7, dtype=torch.int32, device="cuda"), 16, -7)
+    w, wb = ops_ref.guarded(torch.full((T, k), 7.0, device="cuda"), 16, 7.0)
+    s, sb = ops_ref.guarded(torch.full((T, E), 7.0, device="cuda"), 16, 7.0)
+    moe.moe_select(l, ids, w, scores=s if spare else None, **kw)
+    for big, v in ((ib, -7), (wb, 7.0), (sb, 7.0)):
+        assert ops_ref.guards_intact(big, 16, v)
+    return ids, w, s
+
+
+def check(l, k, **kw):
+    ids, w, s = run(l, k, **kw)
+    wi, ww, ws = ref.select(l.cpu(), k, **kw)
+    assert torch.equal(ids.cpu(), wi)
+    for got, want in ((w, ww), (s, ws)):
+        # rounded once: half a step, or half of the smallest subnormal
+        assert bool(((got.cpu().double() - want).abs() <= 1.0001 * U * want.abs() + 2.0 ** -149).all())
+    again = run(l, k, spare=False, **kw)
+    assert torch.equal(ids, again[0]) and torch.equal(w, again[1]) and bool((again[2] == 7.0).all())
+
+
+# (T, E, k, groups, group_k, group_top)
+SHAPES = [
+    (1, 1, 1, 1, 1, 1), (1, 256, 8, 8, 4, 2), (40, 256, 8, 1, 1, 1), (33, 256, 8, 8, 4, 2), (40, 256, 8, 8, 3, 1),
+    (40, 160, 6, 8, 3, 2), (40, 160, 6, 8, 3, 1), (23, 64, 6, 1, 1, 1), (40, 60, 2, 4, 2, 2), (40, 7, 7, 7, 7, 2),
+    (40, 7, 3, 1, 1, 1), (40, 255, 8, 5, 2, 2), (40, 255, 5, 51, 20, 2), (40, 128, 8, 64, 9, 1), (40, 64, 4, 64, 64, 2),
+    (40, 128, 8, 64, 40, 2), (30, 130, 1, 1, 1, 1), (30, 130, 3, 10, 1, 2), (30, 193, 4, 1, 1, 1), (40, 2, 2, 2, 2, 2),
+    (40, 200, 8, 40, 33, 2), (17, 96, 8, 3, 2, 2), (40, 8, 8, 1, 1, 1), (15, 68, 8, 17, 16, 1),
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_select(shape, score, renorm, dtype):
+    T, E, k, groups, group_k, group_top = shape
+    l, _ = ops_ref.guarded(rows(T, E, dtype, E + k), 16, NAN)
+    kw = dict(score=score, renorm=renorm, scale=2.5, groups=groups, group_k=group_k, group_top=group_top)
+    check(l, k, **kw)
+    bias = torch.randn(E, generator=gen(1), device="cuda") * 0.2
+    check(l, k, bias=bias, **kw)
+    bias[::5] = -INF
+    bias[3::7] = NAN
+    bias[1::11] = INF
+    check(l, k, bias=bias, **kw)
+    check(l, k, bias=torch.zeros(E, device="cuda"), **kw)
+
+
+def test_order_of_near_logits_and_choices():
+    """Without a bias the order is that of the logits, however close their scores; with one, differences of 2^-40 count."""
+    l = torch.full((2, 200), -1.0, device="cuda")
+    l[0, 10], l[0, 150] = 60.0, 60.5
+    l[1, 10], l[1, 150] = 1.0, torch.nextafter(torch.tensor(1.0), torch.tensor(2.0))
+    for score in ("softmax", "sigmoid"):
+        ids, _, _ = run(l, 2, score=score)
+        assert ids.tolist() == [[150, 10]] * 2
+    # the least fp32 step of a logit moves its score by 2^-23 s (1 - s)
+    ids, _, _ = run(l[1:], 2, score="sigmoid", bias=torch.full((200,), 0.5, device="cuda"))
+    assert ids.tolist() == [[150, 10]]
+    # -0 and 0 are equal: the lowest id first
+    z = torch.zeros(1, 40, device="cuda")
+    z[0, :20] = -0.0
+    z[0, 3] = 0.0
+    assert run(z, 8, score="sigmoid")[0].tolist() == [list(range(8))]
+
+
+GRADS = [(1, 1, 1), (1, 256, 8), (40, 256, 8), (40, 64, 6), (33, 160, 6), (40, 7, 7), (23, 255, 8), (40, 130, 1),
+         (17, 193, 4), (40, 2, 2), (30, 128, 3)]
+
+
+@pytest.mark.parametrize("shape", GRADS)
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("dtype,dl_dtype,dense", [(F32, F32, True), (F32, BF, False), (BF, F32, False), (BF, BF, True)])
+def test_select_backward(shape, score, renorm, dtype, dl_dtype, dense):
+    T, E, k = shape
+    l, _ = ops_ref.guarded(rows(T, E, dtype, 3 * E + k), 16, NAN)
+    g = gen(E)
+    ids = torch.rand(T, E, generator=g, device="cuda").argsort(1)[:, :k].to(torch.int32).contiguous()
+    if T > 8:
+        ids[3] = int(ids[3, 0])  # one expert in every slot
+        ids[4, 0], ids[5, -1], ids[6, 0] = -1, E, -2 ** 31
+        ids[7] = -1
+    dw = torch.randn(T, k, generator=g, device="cuda")
+    dw[ids < 0] = NAN  # the gradient of a slot without an expert is not looked at
+    ds = torch.randn(T, E, generator=g, device="cuda") * 0.1 if dense else None
+    dl, big = ops_ref.guarded(torch.full((T, E), 7.0, device="cuda", dtype=dl_dtype), 16, 7.0)
+    moe.moe_select_backward(l, ids, dw, dl, score=score, renorm=renorm, scale=2.5, dscores=ds)
+    want, bound = ref.backward(l.cpu(), ids.cpu(), dw.cpu(), score, renorm, 2.5, None if ds is None else ds.cpu())
+    err = (dl.cpu().double() - want).abs()
+    assert not err.isnan().any()
+    bound = bound + ops_ref.HALF[dl_dtype] * (want.abs() + bound)
+    assert bool((err <= bound).all()), (err / bound.clamp(min=1e-300)).max()
+    assert ops_ref.guards_intact(big, 16, 7.0)
+    again = torch.empty_like(dl)
+    moe.moe_select_backward(l, ids, dw, again, score=score, renorm=renorm, scale=2.5, dscores=ds)
+    assert torch.equal(again, dl)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_against_differences(score, renorm):
+    """Directional differences of the kernel's own weights and scores (the choice held: no near ties move it)."""
+    T, E, k = 64, 96, 4
+    g = gen(2)
+    l = torch.randn(T, E, generator=g, device="cuda")
+    l[:, :k] += 8.0  # the chosen ones stand clear
+    dw, ds = torch.randn(T, k, generator=g, device="cuda"), torch.randn(T, E, generator=g, device="cuda")
+    step = torch.randn(T, E, generator=g, device="cuda")
+
+    def loss(x):
+        ids, w, s = run(x, k, score=score, renorm=renorm)
+        at = torch.zeros(T, E, device="cuda", dtype=torch.float64).scatter_(1, ids.long(), w.double())
+        return (at[:, :k] * dw).sum(1) + (s.double() * ds).sum(1)
+
+    ids = torch.arange(k, device="cuda", dtype=torch.int32).repeat(T, 1)
+    dl = torch.empty(T, E, device="cuda")
+    moe.moe_select_backward(l, ids, dw, dl, score=score, renorm=renorm, dscores=ds)
+    h = 2.0 ** -6
+    num = (loss(l + h * step) - loss(l - h * step)) / (2 * h)
+    # fp32 results: up to 100 terms of size <= 4 off by 2^-24 each, over h; third derivative times h^2 / 6
+    assert (num - (dl.double() * step).sum(1)).abs().max() < 400 * U / h + 60 * h * h
+
+
+def test_large_batch_and_empty():
+    """More tokens than one dimension of blocks is wide elsewhere, the last block partly filled; and none."""
+    T, E, k = 300007, 64, 6
+    l = torch.randn(T, E, generator=gen(4), device="cuda")
+    ids, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    moe.moe_select(l, ids, w)
+    top = torch.sort(l, dim=1, descending=True, stable=True)
+    assert torch.equal(ids, top.indices[:, :k].int())
+    want = torch.softmax(top.values[:, :k].double(), 1)
+    assert bool(((w.double() - want).abs() <= 1.0001 * U * want).all())
+    moe.moe_select(l[:0], ids[:0], w[:0])
+    moe.moe_select_backward(l[:0], ids[:0], w[:0], l[:0].clone())
+
+
+def test_past_32_bit_offsets():
+    """Rows behind 4 GiB of logits, scores and gradients."""
+    T, E, k = (1 << 24) - 1, 256, 2
+    tail = 40
+    l = torch.zeros(T, E, dtype=BF, device="cuda")
+    l[-tail:] = rows(tail, E, BF, 9)
+    ids, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    s = torch.empty(T, E, device="cuda")
+    moe.moe_select(l, ids, w, score="sigmoid", scores=s)
+    wi, ww, ws = ref.select(l[-tail:].cpu(), k, "sigmoid")
+    assert torch.equal(ids[-tail:].cpu(), wi) and bool((ids[:-tail] == torch.arange(k, device="cuda")).all())
+    # half a step, or half of the smallest subnormal (scores of e^-400 are among the rows)
+    assert bool(((s[-tail:].cpu().double() - ws).abs() <= 1.0001 * U * ws + 2.0 ** -149).all()) and bool((s[:-tail] == 0.5).all())
+    dl = torch.empty(T, E, device="cuda")
+    moe.moe_select_backward(l, ids, w, dl, score="sigmoid", renorm=False, dscores=s)
+    want, bound = ref.backward(l[-tail:].cpu(), wi, w[-tail:].cpu(), "sigmoid", False, 1.0, s[-tail:].cpu())
+    assert bool(((dl[-tail:].cpu().double() - want).abs() <= bound + U * want.abs()).all())
+
+
+def test_streams_and_graphs():
+    """Two streams at once and a graph replayed among eager work: the results of one call after the other."""
+    T, E, k = 500, 256, 8
+    kw = dict(score="sigmoid", groups=8, group_k=4, group_top=2, scale=2.5)
+    bias = torch.randn(E, generator=gen(6), device="cuda") * 0.1
+    ls = [torch.randn(T, E, generator=gen(7 + i), device="cuda") for i in range(3)]
+    dw = torch.randn(T, k, generator=gen(11), device="cuda")
+
+    def outs():
+        return (torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda"),
+                torch.empty(T, E, device="cuda"))
+
+    def both(l, o, stream=None):
+        moe.moe_select(l, o[0], o[1], bias=bias, stream=stream, **kw)
+        moe.moe_select_backward(l, o[0], dw, o[2], score="sigmoid", scale=2.5, stream=stream)
+
+    want = [outs() for _ in ls]
+    for l, o in zip(ls, want):
+        both(l, o)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in ls], [outs() for _ in ls]
+    for l, o, st in zip(ls, got, streams):
+        both(l, o, st)
+    torch.cuda.synchronize()
+    for o, w in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(o, w))
+    x, o = ls[0].clone(), outs()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        both(x, o)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        both(x, o)
+    for l, w in list(zip(ls, want)) * 2:
+        x.copy_(l)
+        graph.replay()
+        eager = outs()
+        both(ls[1], eager)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(o, w)) and torch.equal(eager[1], want[1][1])
