@@ -438,6 +438,48 @@ moe_status moe_select_backward(const void* logits, int32_t dtype, int64_t T, int
                                const float* dtopk_w, const float* dscores, int32_t dl_dtype,
                                void* dlogits, void* stream);
 
+/* ------------------------------------------------------------ 4-bit integer weights
+ * Weights as whole numbers of 4 bits with a scale per group of G values along K and,
+ * on request, a zero point per group: w = (q - z) * s. Rows are K contiguous:
+ * codes [rows, K/2] (0 .. 15, element 2j in the low nibble), scales [rows, K/G]
+ * (scale_dtype MOE_BF16 or MOE_F32), zeros [rows, K/G] (a byte each; NULL: z = 8).
+ * G is 32, 64 or 128 and divides K.
+ * moe_w4_quantize, for each group v (s by fp32 arithmetic, 1/7 and 1/15 as fp32
+ * numbers, then rounded to scale_dtype):
+ *   without zeros: s = max|v| * (1/7),                     q = rn(v / s) + 8
+ *   with zeros:    s = (max(v, 0) - min(v, 0)) * (1/15),   z = rn(-min(v, 0) / s),
+ *                                                          q = rn(v / s) + z
+ * rn: the nearest whole number to the exact quotient, ties to even; z and q clamped
+ * to [0, 15]. A group whose scale is 0 has codes z (8, or with zeros 0); one with
+ * an infinity or a NaN, or whose scale overflows, too, and scale NaN. x is dtype
+ * (MOE_BF16 or MOE_F32), [B, R, C], with trans = 0 quantised along C into rows
+ * (B, R), with trans = 1 along R into rows (B, C) (C a multiple of 8), as for
+ * moe_mxfp4_quantize and with its limits.
+ * moe_w4_dequantize writes (q - z) * s, formed in fp32 and rounded to dtype, [R, K];
+ * R * K at most 2^35 - 2^11. zeros may hold any byte here and in the product. */
+moe_status moe_w4_quantize(const void* x, int32_t dtype, int32_t trans, int64_t B, int64_t R,
+                           int32_t C, int32_t group, uint8_t* codes, int32_t scale_dtype,
+                           void* scales, uint8_t* zeros, void* stream);
+moe_status moe_w4_dequantize(const uint8_t* codes, int32_t scale_dtype, const void* scales,
+                             const uint8_t* zeros, int64_t R, int32_t K, int32_t group,
+                             int32_t dtype, void* out, void* stream);
+
+/* moe_grouped_gemm of bf16 rows and such weights [E, N, K], codes [E, N, K/2], scales and
+ * zeros [E, N, K/G]:
+ *   out[r] = sum_k a[i(r), k] * w[e, :, k]
+ * Rows, row_index, row_div, M, its limit and the output as moe_grouped_gemm. The
+ * weights are not rounded: codes and zero points meet the rows as whole numbers,
+ * every product exact, in fp32 sums over each group, which join the result times their
+ * scale (fixed order). A row with an infinity or a NaN has any such values in its
+ * results; scales are finite, or NaN for columns of NaN. From one row per expert to
+ * thousands; the input gradient through frozen weights is moe_w4_dequantize and
+ * moe_grouped_gemm with w_trans 0. */
+moe_status moe_w4_grouped_gemm(const void* a, int64_t a_rows, const int32_t* row_index,
+                               int32_t row_div, const uint8_t* w_codes, int32_t scale_dtype,
+                               const void* w_scales, const uint8_t* w_zeros, int32_t group,
+                               int64_t M, int32_t K, int32_t N, int32_t E, const int32_t* offsets,
+                               int32_t out_dtype, void* out, void* stream);
+
 /* ------------------------------------------------------------ measurement
  * Not a step of the layer: the HBM read ceiling its bandwidth-bound kernels
  * are quoted against. Reads `bytes` (a multiple of 16) of device memory at buf

@@ -33,7 +33,7 @@ ENTRY_POINTS = ("moe_status_string", "moe_route_workspace_size", "moe_route",
                 "moe_hbm_read", "moe_grouped_gemm", "moe_grouped_wgrad", "moe_swiglu",
                 "moe_swiglu_backward", "moe_finalize_backward", "moe_mxfp4_scale_stride",
                 "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_grouped_gemm", "moe_select",
-                "moe_select_backward")
+                "moe_select_backward", "moe_w4_quantize", "moe_w4_dequantize", "moe_w4_grouped_gemm")
 
 
 class MoEError(RuntimeError):
@@ -108,6 +108,10 @@ def load_library(path: str = LIB_PATH):
                               ctypes.c_float, _vp, _vp, _vp, _vp]),
         "moe_select_backward": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _i32, ctypes.c_float, _vp,
                                        _vp, _vp, _i32, _vp, _vp]),
+        "moe_w4_quantize": (_i32, [_vp, _i32, _i32, _i64, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _vp]),
+        "moe_w4_dequantize": (_i32, [_vp, _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp]),
+        "moe_w4_grouped_gemm": (_i32, [_vp, _i64, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _i64, _i32,
+                                       _i32, _i32, _vp, _i32, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -631,6 +635,76 @@ def moe_select_backward(logits, topk_ids, dtopk_w, dlogits, score="softmax", ren
     dev, (pl, pi, pw, ps, pd) = _arrays(fn, (logits, topk_ids, dtopk_w, dscores, dlogits))
     _run(fn, _lib.moe_select_backward, dev, stream, pl, t_in, T, E, k, kind, 1 if renorm else 0,
          scale, pi, pw, ps, t_out, pd)
+
+
+def _check_w4(fn, codes, scales, zeros, rows, K) -> int:
+    """The group of codes [rows, K/2] and scales (and zeros) [rows, K/G]."""
+    if codes.dtype is not torch.uint8 or K % 32 or codes.shape != (*rows, K // 2):
+        _refuse(fn, "codes must be uint8 [rows, K/2], K a multiple of 32")
+    ss = scales.shape
+    if len(ss) != len(rows) + 1 or ss[:-1] != rows or ss[-1] < 1 or K % ss[-1]:
+        _refuse(fn, "scales must be [rows, K/G]")
+    if zeros is not None and (zeros.dtype is not torch.uint8 or zeros.shape != ss):
+        _refuse(fn, "zeros must be uint8, shaped as scales")
+    return K // ss[-1]
+
+
+def moe_w4_quantize(x, codes, scales, zeros=None, trans: bool = False, stream=None):
+    """4-bit codes of x [..., K] in groups along its last dimension: codes uint8 [..., K/2], scales (bf16 or
+    fp32) [..., K/G], whose shape gives G (32, 64 or 128), and, if given, zero points uint8 [..., K/G]. With
+    trans, x [B, K, C] (or [K, C]) along its middle dimension: codes [B, C, K/2] and so on."""
+    fn = "moe_w4_quantize"
+    sx = x.shape
+    if len(sx) == 2:
+        B, (R, C) = 1, sx
+        rows, K = ((C,), R) if trans else ((R,), C)
+    elif len(sx) == 3:
+        B, R, C = sx
+        rows, K = ((B, C), R) if trans else ((B, R), C)
+    else:
+        _refuse(fn, "x must have two or three dimensions")
+    group = _check_w4(fn, codes, scales, zeros, rows, K)
+    if (C | group) > _I32_MAX:
+        _too_wide(fn)
+    t_in, t_s = _float(x), _float(scales)
+    dev, (px, pc, ps, pz) = _arrays(fn, (x, codes, scales, zeros))
+    _run(fn, _lib.moe_w4_quantize, dev, stream, px, t_in, 1 if trans else 0, B, R, C, group, pc, t_s, ps, pz)
+
+
+def moe_w4_dequantize(codes, scales, out, zeros=None, stream=None):
+    """out [..., K] (bf16 or fp32) = (codes - zeros) * scales (zeros None: 8)."""
+    fn = "moe_w4_dequantize"
+    so = out.shape
+    if not so:
+        _refuse(fn, "out must be [..., K]")
+    K = so[-1]
+    group = _check_w4(fn, codes, scales, zeros, so[:-1], K)
+    if K > _I32_MAX:
+        _too_wide(fn)
+    t_out, t_s = _float(out), _float(scales)
+    dev, (pc, ps, pz, po) = _arrays(fn, (codes, scales, zeros, out))
+    _run(fn, _lib.moe_w4_dequantize, dev, stream, pc, t_s, ps, pz, out.numel() // max(K, 1), K, group, t_out, po)
+
+
+def moe_w4_grouped_gemm(a, w_codes, w_scales, offsets, out, zeros=None, row_index=None, row_div: int = 1,
+                        stream=None):
+    """moe_grouped_gemm of bf16 rows a [rows, K] and 4-bit weights: codes [E, N, K/2], scales [E, N, K/G]
+    and, if given, zero points [E, N, K/G]; out [M, N] bf16 or fp32."""
+    fn = "moe_w4_grouped_gemm"
+    sa, sw, so = a.shape, w_codes.shape, out.shape
+    if len(sa) != 2 or len(sw) != 3 or len(so) != 2:
+        _refuse(fn, "a and out are matrices, w_codes [E, N, K/2]")
+    if a.dtype is not torch.bfloat16:
+        _refuse(fn, "a must be bf16")
+    (rows, K), (M, N), E = sa, so, sw[0]
+    if (K | N | E) > _I32_MAX:
+        _too_wide(fn)
+    group = _check_w4(fn, w_codes, w_scales, zeros, (E, N), K)
+    _check_rows(fn, M, E, offsets, row_index, row_div)
+    t_s, t_out = _float(w_scales), _float(out)
+    dev, (pa, pw, ps, pz, po, pout, pi) = _arrays(fn, (a, w_codes, w_scales, zeros, offsets, out, row_index))
+    _run(fn, _lib.moe_w4_grouped_gemm, dev, stream, pa, rows, pi, row_div, pw, t_s, ps, pz, group, M, K, N, E,
+         po, t_out, pout)
 
 
 # ---------------------------------------------------------------- device plumbing
