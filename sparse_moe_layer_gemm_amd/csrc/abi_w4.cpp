@@ -82,8 +82,8 @@ moe_status moe_w4_grouped_gemm(const void* a, int64_t a_rows, const int32_t* row
                            E, 0, offsets, out, out_dtype == MOE_BF16, false};
   const moe::W4 w{w_codes, w_scales, w_zeros, scale_dtype == MOE_F32, group};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (!moe::w4_stream_fits(g, w)) return MOE_ERR_UNSUPPORTED;
-  return launch_status(moe::launch_w4_stream(g, w, st));
+  return launch_status(moe::w4_prefer_stream(g, w) ? moe::launch_w4_stream(g, w, st)
+                                                   : moe::launch_w4_tile(g, w, st));
 }
 
 }  // extern "C"

@@ -20,7 +20,19 @@ __device__ __forceinline__ u32x4 code_frag(uint32_t d) {
   r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(odd, 512.f, true));
   return r;
 }
-// 8 adjacent bf16 in that order
+// The same in the codes' own order.
+__device__ __forceinline__ u32x4 code_frag_in_order(uint32_t d) {
+  const uint32_t even = d & 0x0F0F0F0Fu, odd = (d >> 4) & 0x0F0F0F0Fu;
+  const int lo = (int)__builtin_amdgcn_perm(odd, even, 0x05010400u);
+  const int hi = (int)__builtin_amdgcn_perm(odd, even, 0x07030602u);
+  u32x4 r;
+  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false));
+  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true));
+  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false));
+  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true));
+  return r;
+}
+// 8 adjacent bf16 in the order of code_frag
 __device__ __forceinline__ u32x4 row_frag(const u32x4& x) {
   u32x4 r;
   r[0] = __builtin_amdgcn_perm(x[1], x[0], 0x05040100u);

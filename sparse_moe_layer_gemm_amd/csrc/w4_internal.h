@@ -22,8 +22,10 @@ hipError_t launch_w4_quantize_cols(const void* x, bool bf16, long long B, int K,
                                    hipStream_t st);
 hipError_t launch_w4_dequantize(const W4& w, long long R, int K, bool bf16, void* out, hipStream_t st);
 
-// Products of bf16 rows (g.a; g.w and g.w_scale are not used) with such weights [E, N, K].
+// Products of bf16 rows (g.a; g.w and g.w_scale are not used) with such weights [E, N, K]: streamed, for experts
+// with few rows, or on 128 x 256 tiles.
 hipError_t launch_w4_stream(const GroupedArgs& g, const W4& w, hipStream_t st);
-bool w4_stream_fits(const GroupedArgs& g, const W4& w);  // whether the scales of 64 columns fit in LDS
+hipError_t launch_w4_tile(const GroupedArgs& g, const W4& w, hipStream_t st);
+bool w4_prefer_stream(const GroupedArgs& g, const W4& w);
 
 }  // namespace moe

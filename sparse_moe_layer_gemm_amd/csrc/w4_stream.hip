@@ -248,7 +248,14 @@ hipError_t launch_g(const GroupedArgs& g, const W4& w, hipStream_t st) {
 
 }  // namespace
 
-bool w4_stream_fits(const GroupedArgs& g, const W4& w) { return table_bytes(g, w) <= 64 * 1024; }
+bool w4_prefer_stream(const GroupedArgs& g, const W4& w) {
+  if (table_bytes(g, w) > 64 * 1024) return false;
+#ifdef W4_FORCE
+  return W4_FORCE == 1;
+#endif
+  const long long e = g.E < g.M ? g.E : g.M;
+  return g.M <= 16 * e;
+}
 
 hipError_t launch_w4_stream(const GroupedArgs& g, const W4& w, hipStream_t st) {
   switch (w.group) {

@@ -1,0 +1,443 @@
+// Products of bf16 rows with 4-bit integer weights on the matrix cores for experts
+// with many rows: out[r] = a[i(r)] . w[e], w = (q - z) s in groups of G along the depth.
+//
+// One workgroup of 8 wavefronts (2 x 4) computes a 128 x 256 tile of one expert,
+// 64 x 64 per wavefront (an expert's last tile of at most 64 or 32 rows keeps 32 or
+// 16 per wavefront). Rows come into LDS 64 deep at a time as in grouped_tile.hip
+// (three such pairs of 32-deep steps), codes 256 deep, so that a column's piece is a
+// whole 128-byte line (two stages).
+//
+// The weights are never rounded: codes 0 .. 15 meet the rows as they are, exact in
+// bf16, in sums p = sum q x over one group; at its end s p joins the result in fp32
+// and p starts anew. The zero points take z s t with t = sum x over the group, which
+// an MFMA with ones gives: every wavefront forms t for one of its row tiles (the
+// tiles are numbered so that it is its first), and they meet in LDS behind the next
+// barrier. A wavefront spends 9 vector instructions on 8 codes of a column, whose
+// fragment serves four MFMAs, and two FMAs per result and group.
+//
+// The depth is walked in whole stages: behind its end rows are zeros, codes anything
+// finite, and scales 0.
+// Scales and zero points of the 256 columns are fetched 8 groups ahead, 16 bytes of a
+// column at a time, and stand in LDS as fp32, groups apart.
+#include "w4_common.h"
+
+namespace moe {
+namespace {
+
+constexpr int BM = 128, BN = 256, WAVES = 8, GM = 8;
+constexpr int PAIR = 16384, NSA = 3;         // 128 rows, 64 deep
+constexpr int WST = 32768, W0 = NSA * PAIR;  // 256 columns, 256 deep; two of them
+constexpr int CHUNK = 8 * BN * 4;            // 8 groups of fp32
+constexpr int S0 = W0 + 2 * WST, Z0 = S0 + 2 * CHUNK, X0 = Z0 + 2 * CHUNK;
+constexpr int XS = 2 * BM * 4;  // sums of rows of a pair's one or two groups; four pairs
+constexpr int LDS_BYTES = X0 + 4 * XS;
+constexpr int STRIP = 64 * 128;  // a wavefront's epilogue strip
+static_assert(WAVES * STRIP <= S0 && LDS_BYTES <= 160 * 1024, "LDS");
+
+// granule g of a 128-byte row (or column) sits at g ^ swz(row)
+__device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
+
+template <int OFF>
+__device__ __forceinline__ void lds_put(uint32_t addr, float v) {
+  asm volatile("ds_write_b32 %0, %1 offset:%2" ::"v"(addr), "v"(v), "n"(OFF) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// What one 32-deep step reads: row fragments, and 8 codes of each column tile.
+template <int MT>
+struct Step {
+  u32x4 a[MT];
+  uint32_t w[4];
+};
+template <int MT>
+__device__ __forceinline__ void wait_step(Step<MT>& f) {
+#pragma unroll
+  for (int i = 0; i < MT; ++i) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(f.a[i])::"memory");
+  asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(f.w[0]), "+v"(f.w[1]), "+v"(f.w[2]), "+v"(f.w[3])::"memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_vec(f32x4 (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(v[i])::"memory");
+}
+// Keeps what forms v in its place: the compiler's first pass orders matrix and vector
+// instructions by their operands alone, and would hold many steps' results at once.
+template <int MT>
+__device__ __forceinline__ void keep_here(f32x4 (&v)[MT][4]) {
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    asm volatile("" : "+v"(v[i][0]), "+v"(v[i][1]), "+v"(v[i][2]), "+v"(v[i][3]));
+}
+template <int OFF>
+__device__ __forceinline__ f32x4 lds_f32x4(uint32_t addr) {
+  return __builtin_bit_cast(f32x4, lds_b128<OFF>(addr));
+}
+
+// vectors at any address of their elements
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+
+template <int G, bool SF32, bool Z, int MT>
+__device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uint8_t* smem, const RowTile& t,
+                                          int n0) {
+  constexpr int LA = MT > 2 ? MT / 2 : 1, LB = 4;  // 1 KB loads per wavefront of a pair, of a stage of codes
+  constexpr int GPS = 256 / G;                     // groups per stage
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int wm = wave >> 2, wn = wave & 3;
+  const int ng = g.K / G, nws = (g.K + 255) >> 8;
+  const char* const zeros = reinterpret_cast<const char*>(kZeros);
+
+  // ---- direct loads; alim: pairs that hold the lane's granule. Codes behind a column's end
+  // are others' (or zeros behind the buffer): they meet rows of zeros.
+  const char* ap[LA];
+  int alim[LA];
+#pragma unroll
+  for (int q = 0; q < LA; ++q) {
+    const int row = 8 * (wave * LA + q) + (lane >> 3), lg = (lane & 7) ^ swz(row);
+    const int s = row < 32 * MT && t.m0 + row < t.cnt ? source_row(g, t.lo + t.m0 + row) : -1;
+    ap[q] = static_cast<const char*>(g.a) + ((size_t)(s < 0 ? 0 : s) * g.K + 8 * lg) * 2;
+    alim[q] = s < 0 ? 0 : (g.K - 8 * lg + 63) >> 6;
+  }
+  const int wrow = g.K / 2;
+  const Buffer wbuf = make_buffer(w.codes + ((size_t)t.e * g.N + n0) * wrow, (uint32_t)min(BN, g.N - n0) * wrow);
+  uint32_t woff[2];  // of the wavefront's first and second 8 columns, and 16 further the next
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int c = 8 * (wave * LB + q) + (lane >> 3);
+    woff[q] = (uint32_t)c * wrow + 16 * ((lane & 7) ^ swz(c));
+  }
+  auto issue_a = [&](int p, int slot) {
+    uint8_t* to = smem + slot * PAIR + wave * (LA * 1024);
+#pragma unroll
+    for (int q = 0; q < LA; ++q) dma16(p < alim[q] ? ap[q] + (size_t)p * 128 : zeros, to + q * 1024);
+  };
+  auto issue_w = [&](int s, int slot) {
+    uint8_t* to = smem + W0 + slot * WST + wave * (LB * 1024);
+#pragma unroll
+    for (int q = 0; q < LB; ++q) dma16(wbuf, woff[q & 1] + ((q >> 1) * 16u * wrow + 128u * s), to + q * 1024);
+  };
+
+  // ---- scales (wavefronts 0-3) and zero points (4-7), a column per lane; groups behind the
+  // last count as 0
+  const int col = tid & 255;
+  const size_t first = ((size_t)t.e * g.N + min(n0 + col, g.N - 1)) * ng;
+  // groups 8 c .. 8 c + 7; the last chunk of a longer row starts early, so that none is read
+  // behind the row
+  auto chunk_start = [&](int c) { return min(8 * c, ng - 8); };
+  u32x4 raw[SF32 ? 2 : 1];
+  auto load_chunk = [&](int c) {
+    const size_t at = first + chunk_start(c);
+    if (wave < 4) {
+      const uint8_t* p = static_cast<const uint8_t*>(w.scales) + at * (SF32 ? 4 : 2);
+#pragma unroll
+      for (int i = 0; i < (SF32 ? 2 : 1); ++i) raw[i] = reinterpret_cast<const u32x4_any*>(p)[i];
+    } else if constexpr (Z) {
+      const u32x2 d = *reinterpret_cast<const u32x2_any*>(w.zeros + at);
+      raw[0][0] = d[0], raw[0][1] = d[1];
+    }
+  };
+  auto store_chunk = [&](int c) {
+    const int shift = 8 * c - chunk_start(c);
+    if (wave < 4) {
+      float* to = reinterpret_cast<float*>(smem + S0 + (c & 1) * CHUNK) + col;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = SF32 ? __uint_as_float(raw[SF32 ? i >> 2 : 0][i & 3])
+                             : (i & 1) ? bf16_hi(raw[0][(i >> 1) & 3]) : bf16_lo(raw[0][(i >> 1) & 3]);
+        to[((i - shift) & 7) * BN] = i >= shift ? v : 0.f;
+      }
+    } else if constexpr (Z) {
+      float* to = reinterpret_cast<float*>(smem + Z0 + (c & 1) * CHUNK) + col;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        to[((i - shift) & 7) * BN] = i >= shift ? (float)((raw[0][i >> 2] >> (8 * (i & 3))) & 255u) : 0.f;
+    }
+  };
+  auto short_chunk = [&] {  // a row of fewer than 8 groups
+    if (wave < 4) {
+      float* to = reinterpret_cast<float*>(smem + S0) + col;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        to[i * BN] = i >= ng ? 0.f
+                     : SF32  ? static_cast<const float*>(w.scales)[first + i]
+                             : bf16_bits_to_f32(static_cast<const uint16_t*>(w.scales)[first + i]);
+    } else if constexpr (Z) {
+      float* to = reinterpret_cast<float*>(smem + Z0) + col;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) to[i * BN] = i < ng ? (float)w.zeros[first + i] : 0.f;
+    }
+  };
+
+  // ---- fragment addresses. Row tile i of the wavefront is tile i ^ wn of its 64 (32, 16) rows.
+  const int l16 = lane & 15, kg = lane >> 4;
+  const uint32_t lds0 = (uint32_t)(size_t)(lds_u8*)smem;
+  const int am = wm * 16 * MT, bn = wn * 64;
+  uint32_t arow[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    arow[i] = lds0 + (am + 16 * (i ^ (wn & (MT - 1))) + l16) * 128 + ((kg ^ swz(l16)) << 4);
+  const uint32_t wcol = lds0 + W0 + (bn + l16) * 128 + 4 * kg;
+  const uint32_t scol = lds0 + S0 + (bn + 4 * kg) * 4;
+  const uint32_t xrow = (am + 16 * (wn & (MT - 1)) + l16) * 4;  // of row tile i: ^ 64 i
+
+  // step s (0, 1) of the pair in slot; sub: the step within its stage of codes
+  auto read_step = [&](Step<MT>& f, int slot, int s, int wslot, int sub) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) f.a[i] = lds_b128<0>((arow[i] ^ (s << 6)) + slot * PAIR);
+    const uint32_t at = wcol + wslot * WST + ((sub ^ swz(l16)) << 4);
+    f.w[0] = lds_b32<0>(at), f.w[1] = lds_b32<2048>(at), f.w[2] = lds_b32<4096>(at), f.w[3] = lds_b32<6144>(at);
+  };
+  f32x4 acc[MT][4], p[MT][4], xsum;
+  const f32x4 nought = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = nought;
+  const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  auto mfmas = [&](const Step<MT>& f, bool starts) {
+    xsum = mfma16(ones, f.a[0], starts ? nought : xsum);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u32x4 c = code_frag_in_order(f.w[j]);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) p[i][j] = mfma16(c, f.a[i], starts ? nought : p[i][j]);
+    }
+    keep_here(p);
+  };
+  // a step that is a whole group: each column tile's sums join the result at once
+  auto mfmas_fold = [&](const Step<MT>& f, const f32x4 (&s)[4]) {
+    xsum = mfma16(ones, f.a[0], nought);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u32x4 c = code_frag_in_order(f.w[j]);
+      f32x4 v[MT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) v[i] = mfma16(c, f.a[i], nought);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(s[j][q], v[i][q], acc[i][j][q]);
+    }
+  };
+  // scales (and zero points, from Z0 - S0 on) of group n of stage ws; lane l holds columns
+  // 16 j + 4 (l / 16) + 0..3
+  auto scale_addr = [&](int ws) { return scol + ((GPS * ws >> 3) & 1) * CHUNK + (GPS * ws & 7) * (BN * 4); };
+  auto read_scales = [&](f32x4 (&s)[4], uint32_t at, auto off) {
+    constexpr int O = decltype(off)::value;
+    s[0] = lds_f32x4<O>(at), s[1] = lds_f32x4<O + 64>(at), s[2] = lds_f32x4<O + 128>(at), s[3] = lds_f32x4<O + 192>(at);
+  };
+  auto fold = [&](const f32x4 (&s)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(s[j][q], p[i][j][q], acc[i][j][q]);
+    keep_here(acc);
+  };
+  // less z s t of group n of the stage whose scales are at `at`; -t stands xoff bytes behind xrow
+  auto take_zeros = [&](uint32_t at, auto nn, auto xoff) {
+    constexpr int O = decltype(nn)::value * (BN * 4), X = decltype(xoff)::value;
+    f32x4 s[4], z[4];
+    float t[MT];
+    read_scales(s, at, std::integral_constant<int, O>{});
+    if constexpr (Z) read_scales(z, at + (Z0 - S0), std::integral_constant<int, O>{});
+#pragma unroll
+    for (int i = 0; i < MT; ++i) t[i] = __uint_as_float(lds_b32<X>((xrow ^ (64 * i)) + (lds0 + X0)));
+    wait_vec(s);
+    if constexpr (Z) wait_vec(z);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(t[i])::"memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float c = s[j][q] * (Z ? z[j][q] : 8.f);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i][j][q] = __builtin_fmaf(c, t[i], acc[i][j][q]);
+      }
+    keep_here(acc);
+  };
+
+  // ---- start: the first chunk of scales, two stages of codes, three pairs of rows
+  if (ng >= 8) load_chunk(0);
+  issue_w(0, 0), issue_a(0, 0), issue_a(1, 1), issue_w(1, 1), issue_a(2, 2);
+  if (ng >= 8)
+    store_chunk(0);
+  else
+    short_chunk();
+  reinterpret_cast<float*>(smem + X0 + 3 * XS)[tid & (2 * BM - 1)] = 0.f;
+  wait_lds();
+  wait_loads<2 * LA + LB>();
+  __builtin_amdgcn_s_barrier();
+  Step<MT> f0, f1;
+  read_step(f0, 0, 0, 0, 0);
+  wait_step(f0);
+  int slot = 0;
+  for (int ws = 0; ws < nws; ++ws) {
+    static_for<4>([&](auto qq) {
+      constexpr int Q = decltype(qq)::value;
+      const int pair = 4 * ws + Q;
+      const int next = slot == NSA - 1 ? 0 : slot + 1;
+      constexpr bool START0 = G != 128 || (Q & 1) == 0, START1 = false, END1 = G != 128 || (Q & 1) == 1;
+      constexpr int FIRST = 64 * Q / G;  // the pair's first group within the stage
+      f32x4 s[4];
+      const uint32_t at = scale_addr(ws);
+      constexpr int SECOND = G == 32 ? 1 : 0;
+      constexpr std::integral_constant<int, FIRST * BN * 4> s0{};
+      constexpr std::integral_constant<int, (FIRST + SECOND) * BN * 4> s1{};
+      // step 0, whose fragments are in f0
+      if constexpr (G == 32) {
+        read_scales(s, at, s0);
+        read_step(f1, slot, 1, ws & 1, 2 * Q + 1);
+        wait_vec(s);
+        mfmas_fold(f0, s);
+        keep_here(acc);
+        lds_put<Q * XS>(xrow + (lds0 + X0), -xsum[0]);
+      } else {
+        read_step(f1, slot, 1, ws & 1, 2 * Q + 1);
+        mfmas(f0, START0);
+      }
+      wait_step(f1);
+      // the next pair has landed, for everyone behind the barrier, and everyone has read this one
+      wait_lds();
+      wait_loads<Q == 0 ? LA + LB : LA>();
+      __builtin_amdgcn_s_barrier();
+      if constexpr (G == 32) read_scales(s, at, s1);
+      read_step(f0, next, 0, Q == 3 ? (ws + 1) & 1 : ws & 1, Q == 3 ? 0 : 2 * Q + 2);
+      if constexpr (Q == 3) issue_w(ws + 2, ws & 1);
+      issue_a(pair + NSA, slot);
+      if constexpr (G == 32) {
+        wait_vec(s);
+        mfmas_fold(f1, s);
+        keep_here(acc);
+        lds_put<Q * XS + BM * 4>(xrow + (lds0 + X0), -xsum[0]);
+        wait_step(f0);
+      } else {
+        mfmas(f1, START1);
+        if constexpr (END1) read_scales(s, at, s1);
+        wait_step(f0);
+        if constexpr (END1) {
+          wait_vec(s);
+          lds_put<Q * XS>(xrow + (lds0 + X0), -xsum[0]);
+          fold(s);
+        }
+      }
+      // zero points of the groups that ended in the pair before (of none, at the start)
+      constexpr int R = (Q + 3) & 3, N0 = 64 * R / G;
+      const uint32_t from = Q == 0 ? scale_addr(max(ws - 1, 0)) : at;
+      if constexpr (G != 128 || (R & 1) == 1)
+        take_zeros(from, std::integral_constant<int, N0>{}, std::integral_constant<int, R * XS>{});
+      if constexpr (G == 32)
+        take_zeros(from, std::integral_constant<int, N0 + 1>{}, std::integral_constant<int, R * XS + BM * 4>{});
+      // the next 8 groups' scales: loaded behind pair 0, stored behind pair 2 of their last stage but one
+      constexpr int SPC = 8 / GPS;  // stages per chunk
+      if constexpr (Q == 0) {
+        if ((ws & (SPC - 1)) == SPC - 1 && 8 * (ws / SPC + 1) < ng) load_chunk(ws / SPC + 1);
+      }
+      if constexpr (Q == 2) {
+        if ((ws & (SPC - 1)) == SPC - 1 && 8 * (ws / SPC + 1) < ng) store_chunk(ws / SPC + 1);
+      }
+      slot = next;
+    });
+  }
+  wait_lds();
+  wait_loads<0>();
+  __builtin_amdgcn_s_barrier();
+  {  // zero points of the last pair's groups
+    const uint32_t at = scale_addr(nws - 1);
+    constexpr int N0 = 64 * 3 / G;
+    take_zeros(at, std::integral_constant<int, N0>{}, std::integral_constant<int, 3 * XS>{});
+    if constexpr (G == 32)
+      take_zeros(at, std::integral_constant<int, N0 + 1>{}, std::integral_constant<int, 3 * XS + BM * 4>{});
+  }
+
+  // ---- epilogue: lane l holds row l % 16 of a tile, columns 16 j + 4 (l / 16) + 0..3.
+  // Through the wavefront's strip of LDS (fp32: half of the columns at a time; the rings
+  // lie there, which nobody reads any more), so that a row's columns leave together;
+  // the 16-byte granules are swizzled by row.
+  uint8_t* strip = smem + wave * STRIP;
+  auto fence = [] {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+  auto at = [&](int r, int c) { return strip + r * 128 + ((c ^ ((r >> 1) & 7)) << 4); };
+  if (g.out_bf16) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 v = acc[i][j];
+        *reinterpret_cast<u32x2*>(at(16 * (i ^ (wn & (MT - 1))) + l16, 2 * j + (kg >> 1)) + 8 * (kg & 1)) =
+            u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+      }
+    fence();
+#pragma unroll
+    for (int x = 0; x < 2 * MT; ++x) {
+      const int r = 8 * x + (lane >> 3), c = lane & 7, m = t.m0 + am + r, n = n0 + bn + 8 * c;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(at(r, c));
+      if (m < t.cnt && n < g.N)
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.out) + ((size_t)t.lo + m) * g.N + n) = v;
+    }
+  } else {
+    static_for<2>([&](auto hh) {
+      constexpr int h = decltype(hh)::value;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<f32x4*>(at(16 * (i ^ (wn & (MT - 1))) + l16, 4 * j + kg)) = acc[i][2 * h + j];
+      fence();
+#pragma unroll
+      for (int x = 0; x < 2 * MT; ++x) {
+        const int r = 8 * x + (lane >> 3), c = lane & 7, m = t.m0 + am + r, n = n0 + bn + 32 * h + 4 * c;
+        const f32x4 v = *reinterpret_cast<const f32x4*>(at(r, c));
+        if (m < t.cnt && n < g.N)
+          __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(static_cast<float*>(g.out) +
+                                                                  ((size_t)t.lo + m) * g.N + n));
+      }
+      fence();
+    });
+  }
+}
+
+template <int G, bool SF32, bool Z>
+__global__ __launch_bounds__(64 * WAVES, 1) void w4_tile_kernel(GroupedArgs g, W4 w, int nt) {
+  __shared__ __align__(1024) uint8_t smem[LDS_BYTES];
+  RowTile t;
+  if (!find_tile<BM, GM>(g, nt, t)) return;
+  const int left = t.cnt - t.m0;
+  if (left > 64)
+    tile_body<G, SF32, Z, 4>(g, w, smem, t, BN * t.nt);
+  else if (left > 32)
+    tile_body<G, SF32, Z, 2>(g, w, smem, t, BN * t.nt);
+  else
+    tile_body<G, SF32, Z, 1>(g, w, smem, t, BN * t.nt);
+}
+
+template <int G, bool SF32, bool Z>
+hipError_t launch(const GroupedArgs& g, const W4& w, hipStream_t st) {
+  const int nt = (g.N + BN - 1) / BN;
+  const long long n = tile_grid(g, BM, nt);
+  if (n * 64 * WAVES >= (1LL << 32)) return hipErrorInvalidValue;
+  w4_tile_kernel<G, SF32, Z><<<(unsigned)n, 64 * WAVES, 0, st>>>(g, w, nt);
+  return hipGetLastError();
+}
+template <int G>
+hipError_t launch_g(const GroupedArgs& g, const W4& w, hipStream_t st) {
+  if (w.scale_f32) return w.zeros ? launch<G, true, true>(g, w, st) : launch<G, true, false>(g, w, st);
+  return w.zeros ? launch<G, false, true>(g, w, st) : launch<G, false, false>(g, w, st);
+}
+
+}  // namespace
+
+hipError_t launch_w4_tile(const GroupedArgs& g, const W4& w, hipStream_t st) {
+  switch (w.group) {
+    case 32: return launch_g<32>(g, w, st);
+    case 64: return launch_g<64>(g, w, st);
+    default: return launch_g<128>(g, w, st);
+  }
+}
+
+}  // namespace moe

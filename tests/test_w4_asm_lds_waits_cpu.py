@@ -9,7 +9,7 @@ import pytest
 from sparse_moe_layer_gemm_amd import build as pkg_build
 from tests.test_asm_lds_waits_cpu import unsafe_asm_lds_reads
 
-FILES = ["w4_stream.hip"]
+FILES = ["w4_stream.hip", "w4_tile.hip"]
 
 
 @pytest.mark.parametrize("src", FILES)
