@@ -10,7 +10,6 @@ namespace {
 // 8 codes (one dword, element 2j in the low nibble of byte j) -> their values 0 .. 15 as
 // bf16, in the order 0 2 4 6 1 3 5 7: a byte 0 .. 15 read as E4M3 is the code times 2^-9
 // (subnormal up to 7, the first binade from 8), and the converter takes a power of two.
-typedef short i16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ u32x4 code_frag(uint32_t d) {
   const int even = (int)(d & 0x0F0F0F0Fu), odd = (int)((d >> 4) & 0x0F0F0F0Fu);
   u32x4 r;
@@ -20,16 +19,17 @@ __device__ __forceinline__ u32x4 code_frag(uint32_t d) {
   r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(odd, 512.f, true));
   return r;
 }
-// The same in the codes' own order.
+// Four codes, a byte each, as two pairs of bf16.
+__device__ __forceinline__ void code_pairs(u32x4& r, uint32_t bytes, int at) {
+  r[at] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)bytes, 512.f, false));
+  r[at + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)bytes, 512.f, true));
+}
+// The same as code_frag in the codes' own order.
 __device__ __forceinline__ u32x4 code_frag_in_order(uint32_t d) {
   const uint32_t even = d & 0x0F0F0F0Fu, odd = (d >> 4) & 0x0F0F0F0Fu;
-  const int lo = (int)__builtin_amdgcn_perm(odd, even, 0x05010400u);
-  const int hi = (int)__builtin_amdgcn_perm(odd, even, 0x07030602u);
   u32x4 r;
-  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false));
-  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true));
-  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false));
-  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true));
+  code_pairs(r, __builtin_amdgcn_perm(odd, even, 0x05010400u), 0);
+  code_pairs(r, __builtin_amdgcn_perm(odd, even, 0x07030602u), 2);
   return r;
 }
 // 8 adjacent bf16 in the order of code_frag

@@ -1,13 +1,14 @@
 // Products of bf16 rows with 4-bit integer weights for experts with few rows:
 // out[r] = a[i(r)] . w[e], w = (q - z) s in groups of G along the depth.
 //
-// Bound by the stream of codes, and built like grouped_stream.hip: a workgroup takes
-// 64 columns of one expert and up to 16 of its rows, its wavefronts a part of the
-// depth each, through private rings of LDS stages filled by direct loads of whole
-// 128-byte lines (256 codes of a column) without a barrier until the end.
-// The rows come through the same ring, two per load, as many as there are; the
-// scales and zero points of the 64 columns, contiguous over the whole depth, are
-// copied to LDS at the start.
+// Bound by the stream of codes. A workgroup takes 64 columns of one expert and up to 8 or 16
+// of its rows, its wavefronts a part of the depth each. A wavefront has one stage in LDS,
+// 256 deep, filled by direct loads of whole 128-byte lines: it waits for it, reads all of it
+// into registers, sends for the next and multiplies while that is on its way, without a
+// barrier until the end. (Two stages per wavefront hold twice the LDS for fewer wavefronts:
+// 16 tokens through 88 of 256 experts 84 us, so 73-77.) The rows come with the codes, two per
+// load, as many as there are; the scales and zero points of the 64 columns, contiguous over the
+// whole depth, are copied to LDS at the start.
 //
 // Codes 0 .. 15 go to the matrix cores as they are (exact in bf16, like every
 // product): over a group they sum to p = sum q x, one more MFMA with ones gives
@@ -19,8 +20,9 @@
 namespace moe {
 namespace {
 
-constexpr int BN = 64, BM = 16;
-constexpr int WB = 8192, AB = 8192, STAGE = WB + AB;  // 256 deep: 64 columns of codes, 16 rows
+constexpr int BN = 64, kLds = 160 * 1024;
+constexpr int WB = 8192;  // 256 deep: 64 columns of codes; then up to RM rows, 512 bytes each
+constexpr int stage_bytes(int rm) { return WB + 512 * rm; }
 
 // granule g (of 8) of a column's 128 bytes sits at g ^ swz(column), granule g (of 32) of a
 // row's 512 bytes at g ^ row
@@ -63,23 +65,30 @@ __device__ __forceinline__ void wait_stage(Stage<G>& f) {
 }
 
 // One wavefront's part of the depth: stages kb .. ke of the tile's rows, 2 RX of them in LDS.
-template <int G, bool SF32, bool Z, int WV, int D, int RX>
-__device__ __forceinline__ void stream_part(const GroupedArgs& g, const W4& w, const RowTile& t, uint8_t* ring,
+template <int G, bool SF32, bool Z, int RX>
+__device__ __forceinline__ void stream_part(const GroupedArgs& g, const W4& w, const RowTile& t, uint8_t* stage,
                                             uint32_t table, uint32_t ztable, int kb, int ke, int n0,
                                             f32x4 (&acc)[4]) {
-  constexpr int LOADS = 8 + RX, GROUPS = 256 / G, PER = G / 32;
+  constexpr int GROUPS = 256 / G, PER = G / 32;
   const int lane = threadIdx.x & 63, l16 = lane & 15, kg = lane >> 4;
   const char* const zeros = reinterpret_cast<const char*>(kZeros);
   const int wrow = g.K / 2, arow = 2 * g.K, ng = g.K / G;
-  const char *wp[8], *ap[RX];
-  int wlim[8], alim[RX];
+  // Codes behind a column's end are others' (or zeros behind the buffer): they meet rows of
+  // zeros. Column c + 16's granules are swizzled as column c's.
+  const Buffer wbuf = make_buffer(w.codes + ((size_t)t.e * g.N + n0) * wrow, (uint32_t)min(BN, g.N - n0) * wrow);
+  uint32_t woff[2];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int c = 8 * q + (lane >> 3), lg = (lane & 7) ^ swz(c);
-    const bool ok = n0 + c < g.N;
-    wp[q] = reinterpret_cast<const char*>(w.codes) + ((size_t)t.e * g.N + (ok ? n0 + c : 0)) * wrow + 16 * lg;
-    wlim[q] = ok ? min(ke, (wrow - 16 * lg + 127) >> 7) : 0;
+  for (int q = 0; q < 2; ++q) {
+    const int c = 8 * q + (lane >> 3);
+    woff[q] = (uint32_t)c * wrow + 16 * ((lane & 7) ^ swz(c));
   }
+  auto issue_w = [&](int kt) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dma16(wbuf, woff[q & 1] + ((q >> 1) * 16u * wrow + 128u * kt), stage + 1024 * q);
+  };
+  issue_w(kb);  // on its way while the rows are looked up
+  const char* ap[RX];
+  int alim[RX];
 #pragma unroll
   for (int q = 0; q < RX; ++q) {
     const int row = 2 * q + (lane >> 5), lg = (lane & 31) ^ row;
@@ -87,34 +96,28 @@ __device__ __forceinline__ void stream_part(const GroupedArgs& g, const W4& w, c
     ap[q] = static_cast<const char*>(g.a) + (size_t)(s < 0 ? 0 : s) * arow + 16 * lg;
     alim[q] = s < 0 ? 0 : min(ke, (arow - 16 * lg + 511) >> 9);
   }
-  auto issue = [&](int kt, int st) {
-    uint8_t* p = ring + st * STAGE;
+  auto issue_a = [&](int kt) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) dma16(kt < wlim[q] ? wp[q] + (size_t)kt * 128 : zeros, p + 1024 * q);
-#pragma unroll
-    for (int q = 0; q < RX; ++q) dma16(kt < alim[q] ? ap[q] + (size_t)kt * 512 : zeros, p + WB + 1024 * q);
+    for (int q = 0; q < RX; ++q) dma16(kt < alim[q] ? ap[q] + (size_t)kt * 512 : zeros, stage + WB + 1024 * q);
   };
-#pragma unroll
-  for (int s = 0; s < D; ++s) issue(kb + s, s);
-  wait_loads<D * LOADS>();  // this wavefront's part of the tables
+  issue_a(kb);
+  wait_loads<8 + RX>();  // this wavefront's part of the tables
   __builtin_amdgcn_s_barrier();
 
   // rows past those in LDS repeat others: nothing looks at their results
   const int row = l16 & (2 * RX - 1);
-  const uint32_t lds0 = (uint32_t)(size_t)(lds_u8*)ring;
+  const uint32_t lds0 = (uint32_t)(size_t)(lds_u8*)stage;
   const uint32_t waddr = lds0 + l16 * 128 + 4 * kg, xaddr = lds0 + WB + row * 512;
   const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-  int st = 0;
   for (int kt = kb; kt < ke; ++kt) {
-    wait_loads<(D - 1) * LOADS>();
+    wait_loads<0>();
     Stage<G> f;
-    const uint32_t off = st * STAGE;
     static_for<8>([&](auto ii) {
       constexpr int i = decltype(ii)::value;
-      f.x[i] = lds_b128<0>(xaddr + off + (((4 * i + kg) ^ row) << 4));
+      f.x[i] = lds_b128<0>(xaddr + (((4 * i + kg) ^ row) << 4));
       static_for<4>([&](auto jj) {
         constexpr int j = decltype(jj)::value;
-        f.w[i][j] = lds_b32<2048 * j>(waddr + off + ((i ^ swz(l16)) << 4));
+        f.w[i][j] = lds_b32<2048 * j>(waddr + ((i ^ swz(l16)) << 4));
       });
     });
     static_for<GROUPS>([&](auto ii) {
@@ -130,18 +133,17 @@ __device__ __forceinline__ void stream_part(const GroupedArgs& g, const W4& w, c
       });
     });
     wait_stage<G, Z>(f);
-    issue(kt + D, st);
-    st = st + 1 == D ? 0 : st + 1;
+    if (kt + 1 < ke) issue_w(kt + 1), issue_a(kt + 1);  // on their way under this stage's products
 #pragma unroll
     for (int i = 0; i < GROUPS; ++i) {
       if (GROUPS * kt + i >= ng) break;  // behind the last group its scales are anything
-      f32x4 p[4], sum = {0.f, 0.f, 0.f, 0.f};
+      f32x4 p[4], t = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = sum;
+      for (int j = 0; j < 4; ++j) p[j] = t;
 #pragma unroll
       for (int h = 0; h < PER; ++h) {
         const u32x4 x = row_frag(f.x[PER * i + h]);
-        sum = mfma16(x, ones, sum);
+        t = mfma16(x, ones, t);
 #pragma unroll
         for (int j = 0; j < 4; ++j) p[j] = mfma16(x, code_frag(f.w[PER * i + h][j]), p[j]);
       }
@@ -150,7 +152,7 @@ __device__ __forceinline__ void stream_part(const GroupedArgs& g, const W4& w, c
         const float s = __uint_as_float(SF32 ? f.s[i][j] : f.s[i][j] << 16);
         const float z = Z ? (float)f.z[i][j] : 8.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[j][q] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[q], p[j][q]), acc[j][q]);
+        for (int q = 0; q < 4; ++q) acc[j][q] = __builtin_fmaf(s, __builtin_fmaf(-z, t[q], p[j][q]), acc[j][q]);
       }
     }
   }
@@ -158,16 +160,18 @@ __device__ __forceinline__ void stream_part(const GroupedArgs& g, const W4& w, c
 }
 
 // Dynamic LDS: the scales of the 64 columns, then their zero points.
-template <int G, bool SF32, bool Z, int WV, int D>
-__global__ __launch_bounds__(64 * WV, 1) void w4_stream_kernel(GroupedArgs g, W4 w, int nt) {
-  __shared__ __align__(1024) uint8_t smem[WV * D * STAGE];
+template <int G, bool SF32, bool Z, int RM, int WV>
+__global__ __launch_bounds__(64 * WV, 2) void w4_stream_kernel(GroupedArgs g, W4 w, int nt) {
+  constexpr int STAGE = stage_bytes(RM);
+  static_assert(RM * 256 <= STAGE, "partial sums reuse the stages");
+  __shared__ __align__(1024) uint8_t smem[WV * STAGE];
   extern __shared__ __align__(1024) uint8_t tables[];
   RowTile t;
-  if (!find_tile<BM, 8>(g, nt, t)) return;
+  if (!find_tile<RM, 8>(g, nt, t)) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int n0 = BN * t.nt, ng = g.K / G;
-  const int nk = (g.K + 255) / 256, per = (nk + WV - 1) / WV;
-  const int kb = wave * per, ke = min(nk, kb + per);
+  const int nk = (g.K + 255) / 256;
+  const int kb = nk * wave / WV, ke = nk * (wave + 1) / WV;
   const char* const zeros = reinterpret_cast<const char*>(kZeros);
 
   constexpr int SB = SF32 ? 4 : 2;
@@ -184,33 +188,39 @@ __global__ __launch_bounds__(64 * WV, 1) void w4_stream_kernel(GroupedArgs g, W4
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const uint32_t table = (uint32_t)(size_t)(lds_u8*)tables;
-  uint8_t* ring = smem + wave * D * STAGE;
+  uint8_t* stage = smem + wave * STAGE;
   const int rows = t.cnt - t.m0;
+  auto part = [&](auto rx) {
+    constexpr int RX = decltype(rx)::value;
+    if constexpr (2 * RX <= RM) stream_part<G, SF32, Z, RX>(g, w, t, stage, table, table + zat, kb, ke, n0, acc);
+  };
   if (rows <= 2)
-    stream_part<G, SF32, Z, WV, D, 1>(g, w, t, ring, table, table + zat, kb, ke, n0, acc);
+    part(std::integral_constant<int, 1>{});
   else if (rows <= 4)
-    stream_part<G, SF32, Z, WV, D, 2>(g, w, t, ring, table, table + zat, kb, ke, n0, acc);
-  else if (rows <= 8)
-    stream_part<G, SF32, Z, WV, D, 4>(g, w, t, ring, table, table + zat, kb, ke, n0, acc);
+    part(std::integral_constant<int, 2>{});
+  else if (rows <= 8 || RM == 8)
+    part(std::integral_constant<int, 4>{});
   else
-    stream_part<G, SF32, Z, WV, D, 8>(g, w, t, ring, table, table + zat, kb, ke, n0, acc);
+    part(std::integral_constant<int, 8>{});
   __syncthreads();
 
-  // ---- partial sums: wavefront w's at 4 KB w, rows of 64 fp32; lane l holds rows
+  // ---- partial sums: wavefront w's at 256 RM w, rows of 64 fp32; lane l holds rows
   // 4 (l / 16) + 0..3, column 16 j + l % 16
-  float* part = reinterpret_cast<float*>(smem);
+  float* sums = reinterpret_cast<float*>(smem);
   const int l16 = lane & 15, kg = lane >> 4;
+  if (4 * kg < RM) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) part[(wave * 16 + 4 * kg + q) * 64 + 16 * j + l16] = acc[j][q];
+      for (int q = 0; q < 4; ++q) sums[(wave * RM + 4 * kg + q) * 64 + 16 * j + l16] = acc[j][q];
+  }
   __syncthreads();
-  for (int id = tid; id < 256; id += 64 * WV) {
+  for (int id = tid; id < 16 * RM; id += 64 * WV) {
     const int r = id >> 4, c = id & 15, n = n0 + 4 * c, m = t.m0 + r;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int x = 0; x < WV; ++x) {
-      const f32x4 p = *reinterpret_cast<const f32x4*>(part + (x * 16 + r) * 64 + 4 * c);
+      const f32x4 p = *reinterpret_cast<const f32x4*>(sums + (x * RM + r) * 64 + 4 * c);
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] += p[q];
     }
@@ -232,29 +242,60 @@ int table_bytes(const GroupedArgs& g, const W4& w) {
   return s + (w.zeros ? (n + 255) & ~255 : 0) + 64;
 }
 
-template <int G, bool SF32, bool Z, int WV, int D>
+// Workgroups of a product at average loads.
+long long groups_of(const GroupedArgs& g, int rm) {
+  const long long e = g.E < g.M ? g.E : g.M;
+  return e * ((g.M + rm * e - 1) / (rm * e)) * ((g.N + BN - 1) / BN);
+}
+
+template <int G, bool SF32, bool Z, int RM, int WV>
 hipError_t launch(const GroupedArgs& g, const W4& w, hipStream_t st) {
-  const int nt = (g.N + BN - 1) / BN;
-  const long long n = tile_grid(g, BM, nt);
-  if (n * 64 * WV >= (1LL << 32)) return hipErrorInvalidValue;
-  w4_stream_kernel<G, SF32, Z, WV, D><<<(unsigned)n, 64 * WV, table_bytes(g, w), st>>>(g, w, nt);
+  const int nt = (g.N + BN - 1) / BN, tables = table_bytes(g, w);
+  const long long n = tile_grid(g, RM, nt);
+  if (n * 64 * WV >= (1LL << 32) || WV * stage_bytes(RM) + tables > kLds) return hipErrorInvalidValue;
+  w4_stream_kernel<G, SF32, Z, RM, WV><<<(unsigned)n, 64 * WV, tables, st>>>(g, w, nt);
   return hipGetLastError();
+}
+// Rows per tile and wavefronts per workgroup. Measured at 5120 x 1536, G = 128, with weights
+// that no cache holds, us (8 x 4: 8 rows, 4 wavefronts):
+//   experts x rows   8 x 4   8 x 2   16 x 4   16 x 2
+//     8 x 1           13.2    17.3    13.1     -
+//    30 x 1           32.7    26.8    32.5     -
+//   100 x 1.3         76.9    76.7    78.1     -       (G = 32: 109, 143, 163)
+//    16 x 8           28.6    26.8    23.0    27.7
+//   180 x 2.8          151     138     150     -
+//   256 x 4            201     180     189     -
+//   256 x 8            277     246     239     218
+//    64 x 32           336     290     216     187     (tiles 184)
+// So: two wavefronts where there are workgroups enough and the tables leave room for five or
+// more of them in a CU's LDS, else four; 16 rows where experts have more than four.
+template <int G, bool SF32, bool Z>
+hipError_t launch_rows(const GroupedArgs& g, const W4& w, hipStream_t st) {
+  const bool wide = g.M > 4LL * (g.E < g.M ? g.E : g.M);
+  const bool many = groups_of(g, wide ? 16 : 8) > 512 && table_bytes(g, w) <= 16 * 1024;
+  if (wide) return many ? launch<G, SF32, Z, 16, 2>(g, w, st) : launch<G, SF32, Z, 16, 4>(g, w, st);
+  return many ? launch<G, SF32, Z, 8, 2>(g, w, st) : launch<G, SF32, Z, 8, 4>(g, w, st);
 }
 template <int G>
 hipError_t launch_g(const GroupedArgs& g, const W4& w, hipStream_t st) {
-  if (w.scale_f32) return w.zeros ? launch<G, true, true, 3, 2>(g, w, st) : launch<G, true, false, 3, 2>(g, w, st);
-  return w.zeros ? launch<G, false, true, 3, 2>(g, w, st) : launch<G, false, false, 3, 2>(g, w, st);
+  if (w.scale_f32) return w.zeros ? launch_rows<G, true, true>(g, w, st) : launch_rows<G, true, false>(g, w, st);
+  return w.zeros ? launch_rows<G, false, true>(g, w, st) : launch_rows<G, false, false>(g, w, st);
 }
 
 }  // namespace
 
+// The streaming kernel or the 128 x 256 tiles? Measured at 5120 x 1536 (one expert: 5120 x 5120),
+// us, streaming against tiles, by experts x rows: 1 x 16 14, 55; 1 x 128 27, 90; 1 x 256 42, 91;
+// 1 x 512 71, 91; 16 x 32 34, 66; 16 x 128 93, 94; 64 x 16 82, 123; 64 x 32 116, 152; 64 x 64 186, 184;
+// 64 x 128 328, 273; 256 x 16 289, 400; 256 x 32 424, 443. So: up to 64 rows per expert, and where the
+// tiles are too few for the CUs; if the scales of 64 columns fit in LDS, and the grid in a launch.
 bool w4_prefer_stream(const GroupedArgs& g, const W4& w) {
-  if (table_bytes(g, w) > 64 * 1024) return false;
+  if (table_bytes(g, w) > 64 * 1024 || tile_grid(g, 8, (g.N + BN - 1) / BN) * 256 >= (1LL << 32)) return false;
 #ifdef W4_FORCE
   return W4_FORCE == 1;
 #endif
   const long long e = g.E < g.M ? g.E : g.M;
-  return g.M <= 16 * e;
+  return g.M <= 64 * e || e * ((g.M + 128 * e - 1) / (128 * e)) * ((g.N + 255) / 256) < 128;
 }
 
 hipError_t launch_w4_stream(const GroupedArgs& g, const W4& w, hipStream_t st) {
