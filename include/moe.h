@@ -407,9 +407,11 @@ moe_status moe_mxfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scale
  *   ids      the k largest choices of the groups that stay, in falling order
  *   weights  w_j = scale * s[id_j], with renorm (1) divided by the sum of the chosen
  *            scores (a sum of zero leaves zeros)
- * Equal groups and equal choices go to the lowest index. Scores and choices are
- * formed in fp64 and choices with a bias compared to 44 bits; the weights are
- * rounded once. An expert whose logit is NaN or -infinity is left out: its score is
+ * Equal groups and equal choices go to the lowest index. Choices are ordered as fp64
+ * arithmetic orders them (with a bias by 44 bits of them), whatever type is used on the way.
+ * Scores are fp32 results (a sigmoid within 10 half steps, a softmax within 36 and what the
+ * rounding of logit - maximum makes of an exponential); the weights are formed from the
+ * chosen logits in fp64 and rounded once (softmax without renorm: with the fp32 sum of all). An expert whose logit is NaN or -infinity is left out: its score is
  * 0, it is never chosen. Nor is one whose bias is NaN or -infinity. Slots for which
  * no expert is left get id -1 and weight 0: moe_permute leaves such pairs without a
  * row and the finalize calls add nothing for them. A logit of +infinity is the limit

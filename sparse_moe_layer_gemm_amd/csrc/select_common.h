@@ -12,10 +12,11 @@ constexpr int kTokens = 16;  // per workgroup of 256 lanes
 constexpr float kNegInf = -__builtin_inff();
 
 // ---- exchanges within a row of 16 lanes
-enum { ROW_XOR1 = 0xB1, ROW_XOR2 = 0x4E, ROW_HALF_MIRROR = 0x141, ROW_MIRROR = 0x140 };
+enum { ROW_XOR1 = 0xB1, ROW_XOR2 = 0x4E, ROW_HALF_MIRROR = 0x141, ROW_MIRROR = 0x140, ROW_NEXT = 0x101 };
+// (ROW_NEXT: the next lane's value, 0 in the last)
 template <int CTRL>
 __device__ __forceinline__ uint32_t row_get(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, CTRL == ROW_NEXT);
 }
 template <int CTRL>
 __device__ __forceinline__ float row_get(float v) {
@@ -50,6 +51,13 @@ __device__ __forceinline__ T row_max(T v) {
   return row_reduce(v, [](T a, T b) { return a > b ? a : b; });
 }
 
+// Writes to LDS before, reads after: among the lanes of a wavefront (a token has one).
+__device__ __forceinline__ void lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---- logits of one row; NaN and what lies outside E count as -infinity
 __device__ __forceinline__ float usable(float x) { return x == x ? x : kNegInf; }
 __device__ __forceinline__ float logit_at(const void* logits, bool bf16, size_t at) {
@@ -82,6 +90,21 @@ __device__ __forceinline__ void load_logits(const void* logits, bool bf16, size_
       for (int q = 0; q < 4; ++q) v[q] = e + q < E ? logit_at(logits, bf16, base + e + q) : kNegInf;
     }
   }
+}
+
+// ---- scores in fp32; errors in half steps, 2^-24 relative
+// e^x for x <= 0 as 2^r 2^f, f = x log2 e - r with log2 e in two parts: off by 4 (2 of the
+// hardware's power, f's roundings).
+__device__ __forceinline__ float exp_neg32(float x) {
+  x = fmaxf(x, -200.f);
+  const float r = __builtin_rintf(x * 1.44269504f);
+  const float f = __builtin_fmaf(x, 1.92596302e-8f, __builtin_fmaf(x, 1.44269504f, -r));
+  return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), (int)r);
+}
+// 1 / (1 + e^-l) from t = e^-|l|: 4 for t, 3 for 1 + t, 2 for its reciprocal, 1 for the product.
+__device__ __forceinline__ float sigmoid32(float l) {
+  const float t = exp_neg32(-fabsf(l));
+  return (l < 0.f ? t : 1.f) * __builtin_amdgcn_rcpf(1.f + t);
 }
 
 // ---- scores in fp64, good to a few units of the last place

@@ -12,7 +12,7 @@ struct SelectArgs {
   int T, E, k;
   const float* bias;  // [E], or null
   int groups, group_k, group_top;
-  int group_size, group_magic;  // set by the launch
+  int group_size, group_magic, lds_stride;  // set by the launch
   float scale;
   int32_t* ids;  // [T, k]
   float* w;      // [T, k]

@@ -1,5 +1,6 @@
 """Plain 64-bit forms of routing by scores and its gradient, one token at a time in Python numbers."""
 import math
+import struct
 
 import torch
 
@@ -12,6 +13,11 @@ def _sig(l):
 
 def _one_minus_sig(l):
     return _sig(-l) if l < INF else 0.0
+
+
+def bits44(x):
+    """x without the last 8 of its 52 fraction bits: what choices with a bias are compared by."""
+    return struct.unpack("d", struct.pack("Q", struct.unpack("Q", struct.pack("d", x))[0] & ~255))[0]
 
 
 def scores_of(logits, score):
@@ -38,7 +44,7 @@ def select(logits, k, score="softmax", bias=None, groups=1, group_k=1, group_top
         if bias is not None:
             b = bias.double().tolist()
             may = [m and x == x and x != -INF for m, x in zip(may, b)]
-            choice = [x + y for x, y in zip(s, b)]
+            choice = [bits44(x + y) if x + y == x + y else x + y for x, y in zip(s, b)]
         left = [e for e in range(E) if may[e]]
         if groups > 1:
             size, value = E // groups, {}

@@ -44,13 +44,25 @@ def run(l, k, spare=True, **kw):
     return ids, w, s
 
 
+def score_bound(l, want, score):
+    """fp32 scores. Sigmoid: e^-|l| 4 half steps, 1 + it 3 more, the reciprocal 2, the product 1. Softmax: logit - maximum rounds
+    by half a step of itself, which the exponential turns into a relative error; the exponential 4, the sum of up to 256
+    terms 16 + 4 and the terms' own errors 8, the quotient and the product 2. Subnormal results: a few times 2^-149."""
+    if score == "sigmoid":
+        return 10 * U * want + 2.0 ** -146
+    x = l.cpu().double().nan_to_num(nan=-INF)
+    far = (x.amax(1, keepdim=True) - x).nan_to_num(nan=0.0).clamp(max=110.0)
+    return (far + 36) * U * want + 2.0 ** -146
+
+
 def check(l, k, **kw):
     ids, w, s = run(l, k, **kw)
     wi, ww, ws = ref.select(l.cpu(), k, **kw)
     assert torch.equal(ids.cpu(), wi)
-    for got, want in ((w, ww), (s, ws)):
-        # rounded once: half a step, or half of the smallest subnormal
-        assert bool(((got.cpu().double() - want).abs() <= 1.0001 * U * want.abs() + 2.0 ** -149).all())
+    assert bool(((s.cpu().double() - ws).abs() <= score_bound(l, ws, kw["score"])).all())
+    # weights are rounded once (half a step, or half of the smallest subnormal), but for the softmax's fp32 sum
+    halves = 36 if kw["score"] == "softmax" and not kw["renorm"] else 1.0001
+    assert bool(((w.cpu().double() - ww).abs() <= halves * U * ww.abs() + 2.0 ** -149).all())
     again = run(l, k, spare=False, **kw)
     assert torch.equal(ids, again[0]) and torch.equal(w, again[1]) and bool((again[2] == 7.0).all())
 
@@ -98,6 +110,27 @@ def test_order_of_near_logits_and_choices():
     z[0, :20] = -0.0
     z[0, 3] = 0.0
     assert run(z, 8, score="sigmoid")[0].tolist() == [list(range(8))]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("groups,group_k", [(1, 1), (8, 3), (16, 5)])
+def test_close_choices(score, dtype, groups, group_k):
+    """Choices a few steps of fp32 apart, on both sides of what fp32 can tell, in rows beside ordinary ones; ranges that
+    32-bit keys do not hold (logits and biases far apart or large)."""
+    T, E, k = 48, 64, 8
+    g = gen(groups)
+    base = torch.randn(T, E, generator=g, device="cuda")
+    steps = torch.randint(-3, 4, (T, E), generator=g, device="cuda").float()
+    l = torch.where(torch.arange(T, device="cuda")[:, None] % 3 == 0, 1.0 + steps * 2.0 ** -23, base)
+    l[1::6] *= 200
+    l[2::6] += 1000
+    l = l.to(dtype)
+    tiny = steps[0] * 2.0 ** -24
+    for bias in (None, tiny, 0.5 + tiny, torch.randn(E, generator=g, device="cuda"), 3 + tiny, 1e4 * tiny, 100 + 10 * steps[1],
+                 torch.where(steps[2] > 0, -1e9, 0.25)):
+        for top in (1, 2):
+            check(l, k, score=score, renorm=True, scale=1.0, bias=bias, groups=groups, group_k=group_k, group_top=top)
 
 
 GRADS = [(1, 1, 1), (1, 256, 8), (40, 256, 8), (40, 64, 6), (33, 160, 6), (40, 7, 7), (23, 255, 8), (40, 130, 1),
@@ -182,8 +215,8 @@ def test_past_32_bit_offsets():
     moe.moe_select(l, ids, w, score="sigmoid", scores=s)
     wi, ww, ws = ref.select(l[-tail:].cpu(), k, "sigmoid")
     assert torch.equal(ids[-tail:].cpu(), wi) and bool((ids[:-tail] == torch.arange(k, device="cuda")).all())
-    # half a step, or half of the smallest subnormal (scores of e^-400 are among the rows)
-    assert bool(((s[-tail:].cpu().double() - ws).abs() <= 1.0001 * U * ws + 2.0 ** -149).all()) and bool((s[:-tail] == 0.5).all())
+    assert bool(((s[-tail:].cpu().double() - ws).abs() <= score_bound(l[-tail:], ws, "sigmoid")).all())
+    assert bool((s[:-tail] == 0.5).all())
     dl = torch.empty(T, E, device="cuda")
     moe.moe_select_backward(l, ids, w, dl, score="sigmoid", renorm=False, dscores=s)
     want, bound = ref.backward(l[-tail:].cpu(), wi, w[-tail:].cpu(), "sigmoid", False, 1.0, s[-tail:].cpu())
