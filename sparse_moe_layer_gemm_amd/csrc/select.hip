@@ -114,6 +114,15 @@ __device__ __forceinline__ void row_top(const T (&v)[N], T none, T (&top)[K]) {
   merge_lanes<ROW_MIRROR>(top);
 }
 
+// the row's largest value
+template <int N>
+__device__ __forceinline__ float row_top1(const float (&x)[N]) {
+  float m = x[0];
+#pragma unroll
+  for (int j = 1; j < N; ++j) m = fmaxf(m, x[j]);
+  return row_reduce(m, [](float a, float b) { return fmaxf(a, b); });
+}
+
 // the expert of value j of a lane, and the slot of its choice in LDS
 __device__ __forceinline__ int expert_of(int i, int j) { return 64 * (j >> 2) + 4 * i + (j & 3); }
 __device__ __forceinline__ int group_of(const SelectArgs& a, int e) { return (e * a.group_magic) >> 16; }
@@ -125,24 +134,38 @@ template <bool BIASED, int N>
 __device__ __forceinline__ uint64_t kept_groups32(const SelectArgs& a, const float (&c)[N], float* lds, int i,
                                                   float m, bool& unsure) {
   float* counts = lds;
-  lds += a.groups;
+  lds += (a.groups + 3) & ~3;
+  const bool fours = (a.group_size & 3) == 0;  // four at a time, groups 4 slots apart
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int e = expert_of(i, j);
-    lds[e + group_of(a, e)] = c[j];
+  for (int c4 = 0; c4 < N / 4; ++c4) {
+    const int e = expert_of(i, 4 * c4);
+    if (fours) {
+      *reinterpret_cast<f32x4*>(lds + e + 4 * group_of(a, e)) = f32x4{c[4 * c4], c[4 * c4 + 1], c[4 * c4 + 2], c[4 * c4 + 3]};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) lds[e + q + group_of(a, e + q)] = c[4 * c4 + q];
+    }
   }
   lds_fence();
   const bool exact = !BIASED && a.group_top == 1;
   const int share = a.groups <= 2 ? 3 : a.groups <= 4 ? 2 : a.groups <= 8 ? 1 : 0;  // 2^share lanes a group
   for (int g0 = 0; g0 < a.groups; g0 += 16 >> share) {
-    const int g = g0 + (i >> share);
+    const int g = g0 + (i >> share), part0 = i & ((1 << share) - 1);
     float one = kNegInf, two = kNegInf;
+    auto take = [&](float v) {
+      two = __builtin_amdgcn_fmed3f(one, two, v);  // the middle one: two <= one
+      one = fmaxf(one, v);
+    };
     if (g < a.groups) {
-      const float* p = lds + g * (a.group_size + 1);
-      for (int j = i & ((1 << share) - 1); j < a.group_size; j += 1 << share) {
-        const float v = p[j];
-        two = __builtin_amdgcn_fmed3f(one, two, v);  // the middle one: two <= one
-        one = fmaxf(one, v);
+      if (fours) {
+        const float* p = lds + g * (a.group_size + 4);
+        for (int j = 4 * part0; j < a.group_size; j += 4 << share) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(p + j);
+          take(v[0]), take(v[1]), take(v[2]), take(v[3]);
+        }
+      } else {
+        const float* p = lds + g * (a.group_size + 1);
+        for (int j = part0; j < a.group_size; j += 1 << share) take(p[j]);
       }
     }
     auto join = [&](float o1, float o2) {
@@ -265,11 +288,14 @@ __device__ __forceinline__ void load_bias(const SelectArgs& a, int i, float (&b)
 
 // The id of slot i (lane i of the row) by 64-bit keys, -1 for none.
 template <int KT, bool BIASED, int N>
-__device__ __forceinline__ int choose64(const SelectArgs& a, const float (&x)[N], double* lds, int i) {
-  float top = x[0];
+__device__ __forceinline__ int choose64(const SelectArgs& a, const float (&logits)[N], double* lds, int i) {
+  float x[N];
 #pragma unroll
-  for (int j = 1; j < N; ++j) top = x[j] > top ? x[j] : top;
-  top = row_max(top);
+  for (int j = 0; j < N; ++j) {
+    x[j] = logits[j];
+    asm volatile("" : "+v"(x[j]));  // or what is computed of it on the other way is kept for this one, which is rare
+  }
+  const float top = row_top1(x);
   const double m = top == kNegInf ? 0.0 : wide(top);
   double v[N];
   if constexpr (BIASED) {
@@ -319,10 +345,8 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a) {
   load_logits<CH>(a.logits, a.bf16, t, a.E, i, x);
 
   // ---- maximum, and the scores where something needs them
-  float m = x[0];
-#pragma unroll
-  for (int j = 1; j < N; ++j) m = x[j] > m ? x[j] : m;
-  m = row_max(m);
+  float m = 0.f;
+  if (!(BIASED && a.sigmoid)) m = row_top1(x);
   float s[N], inverse = 0.f;
   if (BIASED || a.scores || (!a.sigmoid && !a.renorm)) {
     if (a.sigmoid) {
@@ -369,13 +393,11 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a) {
     load_bias<CH>(a, i, b);
 #pragma unroll
     for (int j = 0; j < N; ++j) c[j] = x[j] == kNegInf ? kNegInf : s[j] + b[j];
-    high = c[0];
-#pragma unroll
-    for (int j = 1; j < N; ++j) high = c[j] > high ? c[j] : high;
-    high = row_max(high);
+    high = row_top1(c);
   }
   if ((!exact || a.group_top == 2) && high != kNegInf && !(fabsf(high) <= (BIASED ? 4.f : 0x1p120f))) unsure = true;
   uint32_t v[N];
+  const uint32_t least = exact ? 0x00800000u : 256u;  // keys below stand for none
   if (exact) {
 #pragma unroll
     for (int j = 0; j < N; ++j)  // -0 counts as 0
@@ -384,18 +406,18 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const float units = __builtin_fmaf(c[j] - high, BIASED ? 0x1p23f : 0x1p19f, 0x1p24f - 1.f);
-      v[j] = (uint32_t)fmaxf(units, 1.f) << 8 | (uint32_t)(255 - expert_of(i, j));
+      // 1 at least, but 0 for -infinity: the middle one of units, 1 and a large number (-infinity there)
+      const float clamped = __builtin_amdgcn_fmed3f(units, 1.f, __builtin_fmaf(c[j], 0x1p-30f, 0x1p100f));
+      v[j] = (uint32_t)clamped << 8 | (uint32_t)(255 - expert_of(i, j));
     }
   }
-#pragma unroll
-  for (int j = 0; j < N; ++j) v[j] = c[j] == kNegInf ? 0u : v[j];
   if (a.groups > 1)
     drop_groups(a, kept_groups32<BIASED>(a, c, reinterpret_cast<float*>(own), i, m, unsure), i, v, 0u);
   uint32_t top[KT], mine = 0;
   row_top<KT>(v, 0u, top);
 #pragma unroll
   for (int j = 0; j < KT; ++j) mine = i == j ? top[j] : mine;
-  if (i >= a.k) mine = 0;
+  if (i >= a.k || mine < least) mine = 0;
   int id = mine ? 255 - (int)(mine & 255u) : -1;
   if (!exact) {
     // the chosen ones D apart, nothing else within D of the last, and all inside the range of 24 bits
@@ -454,8 +476,10 @@ hipError_t launch_select(SelectArgs a, hipStream_t st) {
   const unsigned grid = (unsigned)((a.T + kTokens - 1) / kTokens);
   a.group_size = a.E / a.groups;
   a.group_magic = (65536 + a.group_size - 1) / a.group_size;  // e * magic >> 16 = e / group_size for e < 256
-  const int most = (a.E + 63) / 64 * 64;  // experts that the lanes hold, a slot free after each group of them
-  a.lds_stride = a.groups + most + (most - 1) / a.group_size;
+  // The lanes hold `most` experts, a slot free after each group of them; at least 2 (mod 4), for vectors and banks.
+  // The fp32 choices, four slots free after each group of four or more, take less.
+  const int most = (a.E + 63) / 64 * 64;
+  a.lds_stride = (a.groups + most + (most - 1) / a.group_size + 1) / 4 * 4 + 2;
   const size_t lds = a.groups > 1 ? sizeof(double) * kTokens * a.lds_stride : 0;
   switch ((a.E + 63) / 64) {
     case 1: return launch_k<1>(a, grid, lds, st);
