@@ -23,7 +23,7 @@ hipError_t launch_w4_quantize_cols(const void* x, bool bf16, long long B, int K,
 hipError_t launch_w4_dequantize(const W4& w, long long R, int K, bool bf16, void* out, hipStream_t st);
 
 // Products of bf16 rows (g.a; g.w and g.w_scale are not used) with such weights [E, N, K]: streamed, for experts
-// with few rows, or on 128 x 256 tiles.
+// with few rows, or on tiles.
 hipError_t launch_w4_stream(const GroupedArgs& g, const W4& w, hipStream_t st);
 hipError_t launch_w4_tile(const GroupedArgs& g, const W4& w, hipStream_t st);
 bool w4_prefer_stream(const GroupedArgs& g, const W4& w);

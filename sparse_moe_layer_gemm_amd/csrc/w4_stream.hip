@@ -284,18 +284,15 @@ hipError_t launch_g(const GroupedArgs& g, const W4& w, hipStream_t st) {
 
 }  // namespace
 
-// The streaming kernel or the 128 x 256 tiles? Measured at 5120 x 1536 (one expert: 5120 x 5120),
-// us, streaming against tiles, by experts x rows: 1 x 16 14, 55; 1 x 128 27, 90; 1 x 256 42, 91;
-// 1 x 512 71, 91; 16 x 32 34, 66; 16 x 128 93, 94; 64 x 16 82, 123; 64 x 32 116, 152; 64 x 64 186, 184;
-// 64 x 128 328, 273; 256 x 16 289, 400; 256 x 32 424, 443. So: up to 64 rows per expert, and where the
-// tiles are too few for the CUs; if the scales of 64 columns fit in LDS, and the grid in a launch.
+// The streaming kernel or tiles? Measured at 5120 x 1536 (one expert: 5120 x 5120), G = 128, us, streaming
+// against the faster tiles, by experts x rows: 1 x 16 14, 32; 1 x 128 28, 47; 1 x 256 41, 47; 1 x 512 70, 58;
+// 16 x 32 34, 48; 16 x 64 57, 60; 16 x 128 90, 61; 64 x 16 80, 97; 64 x 32 112, 110; 64 x 64 179, 148;
+// 256 x 16 276, 301; 256 x 32 405, 351; 48 x 42 at 1440 x 2056, G = 32: 94, 75. So: below 32 rows per expert, and
+// where the tiles are too few for the CUs; if the scales of 64 columns fit in LDS, and the grid in a launch.
 bool w4_prefer_stream(const GroupedArgs& g, const W4& w) {
   if (table_bytes(g, w) > 64 * 1024 || tile_grid(g, 8, (g.N + BN - 1) / BN) * 256 >= (1LL << 32)) return false;
-#ifdef W4_FORCE
-  return W4_FORCE == 1;
-#endif
   const long long e = g.E < g.M ? g.E : g.M;
-  return g.M <= 64 * e || e * ((g.M + 128 * e - 1) / (128 * e)) * ((g.N + 255) / 256) < 128;
+  return g.M < 32 * e || e * ((g.M + 64 * e - 1) / (64 * e)) * ((g.N + 127) / 128) <= 192;
 }
 
 hipError_t launch_w4_stream(const GroupedArgs& g, const W4& w, hipStream_t st) {

@@ -1,11 +1,11 @@
 // Products of bf16 rows with 4-bit integer weights on the matrix cores for experts
 // with many rows: out[r] = a[i(r)] . w[e], w = (q - z) s in groups of G along the depth.
 //
-// One workgroup of 8 wavefronts (2 x 4) computes a 128 x 256 tile of one expert,
-// 64 x 64 per wavefront (an expert's last tile of at most 64 or 32 rows keeps 32 or
-// 16 per wavefront). Rows come into LDS 64 deep at a time as in grouped_tile.hip
-// (three such pairs of 32-deep steps), codes 256 deep, so that a column's piece is a
-// whole 128-byte line (two stages).
+// A wavefront computes up to 64 rows x 64 or 32 columns of one expert (32 or 16 rows where
+// an expert's last tile has no more); 2 x 4 of the former make a 128 x 256 tile, one to a
+// CU, 1 x 4 of the latter a 64 x 128 tile, two to a CU. Rows come into LDS 64 deep at a
+// time as in grouped_tile.hip (three such pairs of 32-deep steps; four gain 2 %), codes
+// 256 deep, so that a column's piece is a whole 128-byte line (two stages).
 //
 // The weights are never rounded: codes 0 .. 15 meet the rows as they are, exact in
 // bf16, in sums p = sum q x over one group; at its end s p joins the result in fp32
@@ -17,22 +17,28 @@
 //
 // The depth is walked in whole stages: behind its end rows are zeros, codes anything
 // finite, and scales 0.
-// Scales and zero points of the 256 columns are fetched 8 groups ahead, 16 bytes of a
+// Scales and zero points of the tile's columns are fetched 8 groups ahead, 16 bytes of a
 // column at a time, and stand in LDS as fp32, groups apart.
 #include "w4_common.h"
 
 namespace moe {
 namespace {
 
-constexpr int BM = 128, BN = 256, WAVES = 8, GM = 8;
-constexpr int PAIR = 16384, NSA = 3;         // 128 rows, 64 deep
-constexpr int WST = 32768, W0 = NSA * PAIR;  // 256 columns, 256 deep; two of them
-constexpr int CHUNK = 8 * BN * 4;            // 8 groups of fp32
-constexpr int S0 = W0 + 2 * WST, Z0 = S0 + 2 * CHUNK, X0 = Z0 + 2 * CHUNK;
-constexpr int XS = 2 * BM * 4;  // sums of rows of a pair's one or two groups; four pairs
-constexpr int LDS_BYTES = X0 + 4 * XS;
-constexpr int STRIP = 64 * 128;  // a wavefront's epilogue strip
-static_assert(WAVES * STRIP <= S0 && LDS_BYTES <= 160 * 1024, "LDS");
+constexpr int GM = 8, NSA = 3;
+// WM x 4 wavefronts, each of up to 64 rows and 16 NJ columns
+template <int WM_, int NJ_>
+struct Shape {
+  static constexpr int WM = WM_, NJ = NJ_, WAVES = 4 * WM, BM = 64 * WM, BN = 64 * NJ;
+  static constexpr int PAIR = BM * 128;                // rows, 64 deep; NSA of them
+  static constexpr int WST = BN * 128, W0 = NSA * PAIR;  // columns, 256 deep; two of them
+  static constexpr int CHUNK = 8 * BN * 4;             // 8 groups of fp32
+  static constexpr int S0 = W0 + 2 * WST, Z0 = S0 + 2 * CHUNK, X0 = Z0 + 2 * CHUNK;
+  static constexpr int XS = 2 * BM * 4;  // sums of rows of a pair's one or two groups; four pairs
+  static constexpr int LDS_BYTES = X0 + 4 * XS;
+  static constexpr int STRIP = 64 * 128;  // a wavefront's epilogue strip
+  static_assert(BN == 32 * WAVES, "a lane loads a column's scales or zero points, a wavefront 32 columns of codes");
+  static_assert(WAVES * STRIP <= S0 && LDS_BYTES <= 160 * 1024, "LDS");
+};
 
 // granule g of a 128-byte row (or column) sits at g ^ swz(row)
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
@@ -44,16 +50,17 @@ __device__ __forceinline__ void lds_put(uint32_t addr, float v) {
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // What one 32-deep step reads: row fragments, and 8 codes of each column tile.
-template <int MT>
+template <int MT, int NJ>
 struct Step {
   u32x4 a[MT];
-  uint32_t w[4];
+  uint32_t w[NJ];
 };
-template <int MT>
-__device__ __forceinline__ void wait_step(Step<MT>& f) {
+template <int MT, int NJ>
+__device__ __forceinline__ void wait_step(Step<MT, NJ>& f) {
 #pragma unroll
   for (int i = 0; i < MT; ++i) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(f.a[i])::"memory");
-  asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(f.w[0]), "+v"(f.w[1]), "+v"(f.w[2]), "+v"(f.w[3])::"memory");
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(f.w[j])::"memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_vec(f32x4 (&v)[N]) {
@@ -62,11 +69,12 @@ __device__ __forceinline__ void wait_vec(f32x4 (&v)[N]) {
 }
 // Keeps what forms v in its place: the compiler's first pass orders matrix and vector
 // instructions by their operands alone, and would hold many steps' results at once.
-template <int MT>
-__device__ __forceinline__ void keep_here(f32x4 (&v)[MT][4]) {
+template <int MT, int NJ>
+__device__ __forceinline__ void keep_here(f32x4 (&v)[MT][NJ]) {
 #pragma unroll
   for (int i = 0; i < MT; ++i)
-    asm volatile("" : "+v"(v[i][0]), "+v"(v[i][1]), "+v"(v[i][2]), "+v"(v[i][3]));
+#pragma unroll
+    for (int j = 0; j < NJ; j += 2) asm volatile("" : "+v"(v[i][j]), "+v"(v[i][j + 1]));
 }
 template <int OFF>
 __device__ __forceinline__ f32x4 lds_f32x4(uint32_t addr) {
@@ -77,9 +85,11 @@ __device__ __forceinline__ f32x4 lds_f32x4(uint32_t addr) {
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 
-template <int G, bool SF32, bool Z, int MT>
+template <class S, int G, bool SF32, bool Z, int MT>
 __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uint8_t* smem, const RowTile& t,
                                           int n0) {
+  constexpr int NJ = S::NJ, BM = S::BM, BN = S::BN, PAIR = S::PAIR, WST = S::WST, W0 = S::W0, CHUNK = S::CHUNK,
+                S0 = S::S0, Z0 = S::Z0, X0 = S::X0, XS = S::XS;
   constexpr int LA = MT > 2 ? MT / 2 : 1, LB = 4;  // 1 KB loads per wavefront of a pair, of a stage of codes
   constexpr int GPS = 256 / G;                     // groups per stage
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -94,7 +104,7 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
 #pragma unroll
   for (int q = 0; q < LA; ++q) {
     const int row = 8 * (wave * LA + q) + (lane >> 3), lg = (lane & 7) ^ swz(row);
-    const int s = row < 32 * MT && t.m0 + row < t.cnt ? source_row(g, t.lo + t.m0 + row) : -1;
+    const int s = row < 16 * MT * S::WM && t.m0 + row < t.cnt ? source_row(g, t.lo + t.m0 + row) : -1;
     ap[q] = static_cast<const char*>(g.a) + ((size_t)(s < 0 ? 0 : s) * g.K + 8 * lg) * 2;
     alim[q] = s < 0 ? 0 : (g.K - 8 * lg + 63) >> 6;
   }
@@ -117,9 +127,9 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
     for (int q = 0; q < LB; ++q) dma16(wbuf, woff[q & 1] + ((q >> 1) * 16u * wrow + 128u * s), to + q * 1024);
   };
 
-  // ---- scales (wavefronts 0-3) and zero points (4-7), a column per lane; groups behind the
+  // ---- scales (the first half of the wavefronts) and zero points, a column per lane; groups behind the
   // last count as 0
-  const int col = tid & 255;
+  const int col = tid & (BN - 1);
   const size_t first = ((size_t)t.e * g.N + min(n0 + col, g.N - 1)) * ng;
   // groups 8 c .. 8 c + 7; the last chunk of a longer row starts early, so that none is read
   // behind the row
@@ -127,7 +137,7 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
   u32x4 raw[SF32 ? 2 : 1];
   auto load_chunk = [&](int c) {
     const size_t at = first + chunk_start(c);
-    if (wave < 4) {
+    if (tid < BN) {
       const uint8_t* p = static_cast<const uint8_t*>(w.scales) + at * (SF32 ? 4 : 2);
 #pragma unroll
       for (int i = 0; i < (SF32 ? 2 : 1); ++i) raw[i] = reinterpret_cast<const u32x4_any*>(p)[i];
@@ -138,7 +148,7 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
   };
   auto store_chunk = [&](int c) {
     const int shift = 8 * c - chunk_start(c);
-    if (wave < 4) {
+    if (tid < BN) {
       float* to = reinterpret_cast<float*>(smem + S0 + (c & 1) * CHUNK) + col;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -154,7 +164,7 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
     }
   };
   auto short_chunk = [&] {  // a row of fewer than 8 groups
-    if (wave < 4) {
+    if (tid < BN) {
       float* to = reinterpret_cast<float*>(smem + S0) + col;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -171,7 +181,7 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
   // ---- fragment addresses. Row tile i of the wavefront is tile i ^ wn of its 64 (32, 16) rows.
   const int l16 = lane & 15, kg = lane >> 4;
   const uint32_t lds0 = (uint32_t)(size_t)(lds_u8*)smem;
-  const int am = wm * 16 * MT, bn = wn * 64;
+  const int am = wm * 16 * MT, bn = wn * 16 * NJ;
   uint32_t arow[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -181,23 +191,23 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
   const uint32_t xrow = (am + 16 * (wn & (MT - 1)) + l16) * 4;  // of row tile i: ^ 64 i
 
   // step s (0, 1) of the pair in slot; sub: the step within its stage of codes
-  auto read_step = [&](Step<MT>& f, int slot, int s, int wslot, int sub) {
+  auto read_step = [&](Step<MT, NJ>& f, int slot, int s, int wslot, int sub) {
 #pragma unroll
     for (int i = 0; i < MT; ++i) f.a[i] = lds_b128<0>((arow[i] ^ (s << 6)) + slot * PAIR);
     const uint32_t at = wcol + wslot * WST + ((sub ^ swz(l16)) << 4);
-    f.w[0] = lds_b32<0>(at), f.w[1] = lds_b32<2048>(at), f.w[2] = lds_b32<4096>(at), f.w[3] = lds_b32<6144>(at);
+    static_for<NJ>([&](auto jj) { f.w[decltype(jj)::value] = lds_b32<2048 * decltype(jj)::value>(at); });
   };
-  f32x4 acc[MT][4], p[MT][4], xsum;
+  f32x4 acc[MT][NJ], p[MT][NJ], xsum;
   const f32x4 nought = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = nought;
+    for (int j = 0; j < NJ; ++j) acc[i][j] = nought;
   const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-  auto mfmas = [&](const Step<MT>& f, bool starts) {
+  auto mfmas = [&](const Step<MT, NJ>& f, bool starts) {
     xsum = mfma16(ones, f.a[0], starts ? nought : xsum);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NJ; ++j) {
       const u32x4 c = code_frag_in_order(f.w[j]);
 #pragma unroll
       for (int i = 0; i < MT; ++i) p[i][j] = mfma16(c, f.a[i], starts ? nought : p[i][j]);
@@ -205,10 +215,10 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
     keep_here(p);
   };
   // a step that is a whole group: each column tile's sums join the result at once
-  auto mfmas_fold = [&](const Step<MT>& f, const f32x4 (&s)[4]) {
+  auto mfmas_fold = [&](const Step<MT, NJ>& f, const f32x4 (&s)[NJ]) {
     xsum = mfma16(ones, f.a[0], nought);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < NJ; ++j) {
       const u32x4 c = code_frag_in_order(f.w[j]);
       f32x4 v[MT];
 #pragma unroll
@@ -222,13 +232,13 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
   // scales (and zero points, from Z0 - S0 on) of group n of stage ws; lane l holds columns
   // 16 j + 4 (l / 16) + 0..3
   auto scale_addr = [&](int ws) { return scol + ((GPS * ws >> 3) & 1) * CHUNK + (GPS * ws & 7) * (BN * 4); };
-  auto read_scales = [&](f32x4 (&s)[4], uint32_t at, auto off) {
+  auto read_scales = [&](f32x4 (&s)[NJ], uint32_t at, auto off) {
     constexpr int O = decltype(off)::value;
-    s[0] = lds_f32x4<O>(at), s[1] = lds_f32x4<O + 64>(at), s[2] = lds_f32x4<O + 128>(at), s[3] = lds_f32x4<O + 192>(at);
+    static_for<NJ>([&](auto jj) { s[decltype(jj)::value] = lds_f32x4<O + 64 * decltype(jj)::value>(at); });
   };
-  auto fold = [&](const f32x4 (&s)[4]) {
+  auto fold = [&](const f32x4 (&s)[NJ]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -238,7 +248,7 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
   // less z s t of group n of the stage whose scales are at `at`; -t stands xoff bytes behind xrow
   auto take_zeros = [&](uint32_t at, auto nn, auto xoff) {
     constexpr int O = decltype(nn)::value * (BN * 4), X = decltype(xoff)::value;
-    f32x4 s[4], z[4];
+    f32x4 s[NJ], z[NJ];
     float t[MT];
     read_scales(s, at, std::integral_constant<int, O>{});
     if constexpr (Z) read_scales(z, at + (Z0 - S0), std::integral_constant<int, O>{});
@@ -249,7 +259,7 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
 #pragma unroll
     for (int i = 0; i < MT; ++i) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(t[i])::"memory");
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float c = s[j][q] * (Z ? z[j][q] : 8.f);
@@ -270,7 +280,7 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
   wait_lds();
   wait_loads<2 * LA + LB>();
   __builtin_amdgcn_s_barrier();
-  Step<MT> f0, f1;
+  Step<MT, NJ> f0, f1;
   read_step(f0, 0, 0, 0, 0);
   wait_step(f0);
   int slot = 0;
@@ -281,7 +291,7 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
       const int next = slot == NSA - 1 ? 0 : slot + 1;
       constexpr bool START0 = G != 128 || (Q & 1) == 0, START1 = false, END1 = G != 128 || (Q & 1) == 1;
       constexpr int FIRST = 64 * Q / G;  // the pair's first group within the stage
-      f32x4 s[4];
+      f32x4 s[NJ];
       const uint32_t at = scale_addr(ws);
       constexpr int SECOND = G == 32 ? 1 : 0;
       constexpr std::integral_constant<int, FIRST * BN * 4> s0{};
@@ -356,7 +366,7 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
   // Through the wavefront's strip of LDS (fp32: half of the columns at a time; the rings
   // lie there, which nobody reads any more), so that a row's columns leave together;
   // the 16-byte granules are swizzled by row.
-  uint8_t* strip = smem + wave * STRIP;
+  uint8_t* strip = smem + wave * S::STRIP;
   auto fence = [] {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -367,21 +377,22 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         const f32x4 v = acc[i][j];
         *reinterpret_cast<u32x2*>(at(16 * (i ^ (wn & (MT - 1))) + l16, 2 * j + (kg >> 1)) + 8 * (kg & 1)) =
             u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
       }
     fence();
+    constexpr int GR = 2 * NJ;  // granules of a row
 #pragma unroll
-    for (int x = 0; x < 2 * MT; ++x) {
-      const int r = 8 * x + (lane >> 3), c = lane & 7, m = t.m0 + am + r, n = n0 + bn + 8 * c;
+    for (int x = 0; x < 16 * MT * GR / 64; ++x) {
+      const int r = 64 / GR * x + lane / GR, c = lane % GR, m = t.m0 + am + r, n = n0 + bn + 8 * c;
       const u32x4 v = *reinterpret_cast<const u32x4*>(at(r, c));
       if (m < t.cnt && n < g.N)
         *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.out) + ((size_t)t.lo + m) * g.N + n) = v;
     }
   } else {
-    static_for<2>([&](auto hh) {
+    static_for<NJ / 2>([&](auto hh) {
       constexpr int h = decltype(hh)::value;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -402,32 +413,49 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
   }
 }
 
-template <int G, bool SF32, bool Z>
-__global__ __launch_bounds__(64 * WAVES, 1) void w4_tile_kernel(GroupedArgs g, W4 w, int nt) {
-  __shared__ __align__(1024) uint8_t smem[LDS_BYTES];
+template <class S, int G, bool SF32, bool Z>
+__global__ __launch_bounds__(64 * S::WAVES, 2 / S::WM) void w4_tile_kernel(GroupedArgs g, W4 w, int nt) {
+  __shared__ __align__(1024) uint8_t smem[S::LDS_BYTES];
   RowTile t;
-  if (!find_tile<BM, GM>(g, nt, t)) return;
+  if (!find_tile<S::BM, GM>(g, nt, t)) return;
   const int left = t.cnt - t.m0;
-  if (left > 64)
-    tile_body<G, SF32, Z, 4>(g, w, smem, t, BN * t.nt);
-  else if (left > 32)
-    tile_body<G, SF32, Z, 2>(g, w, smem, t, BN * t.nt);
+  if (left > S::BM / 2)
+    tile_body<S, G, SF32, Z, 4>(g, w, smem, t, S::BN * t.nt);
+  else if (left > S::BM / 4)
+    tile_body<S, G, SF32, Z, 2>(g, w, smem, t, S::BN * t.nt);
   else
-    tile_body<G, SF32, Z, 1>(g, w, smem, t, BN * t.nt);
+    tile_body<S, G, SF32, Z, 1>(g, w, smem, t, S::BN * t.nt);
 }
 
-template <int G, bool SF32, bool Z>
+template <class S, int G, bool SF32, bool Z>
 hipError_t launch(const GroupedArgs& g, const W4& w, hipStream_t st) {
-  const int nt = (g.N + BN - 1) / BN;
-  const long long n = tile_grid(g, BM, nt);
-  if (n * 64 * WAVES >= (1LL << 32)) return hipErrorInvalidValue;
-  w4_tile_kernel<G, SF32, Z><<<(unsigned)n, 64 * WAVES, 0, st>>>(g, w, nt);
+  const int nt = (g.N + S::BN - 1) / S::BN;
+  const long long n = tile_grid(g, S::BM, nt);
+  if (n * 64 * S::WAVES >= (1LL << 32)) return hipErrorInvalidValue;
+  w4_tile_kernel<S, G, SF32, Z><<<(unsigned)n, 64 * S::WAVES, 0, st>>>(g, w, nt);
   return hipGetLastError();
+}
+// Tiles at average loads.
+long long tiles_of(const GroupedArgs& g, int bm, int bn) {
+  const long long e = g.E < g.M ? g.E : g.M;
+  return e * ((g.M + bm * e - 1) / (bm * e)) * ((g.N + bn - 1) / bn);
+}
+// Which tile? 512 small ones take 0.56 of 256 large ones' time where both fill the CUs, so the
+// shape with fewer rounds at those weights. Measured at 5120 x 1536, G = 128, us, large against
+// small, experts x rows: 64 x 64 181, 148; 64 x 128 267, 220; 64 x 256 357, 375; 64 x 512 619, 696;
+// 256 x 128 830, 813; 16 x 128 92, 61; one expert, 5120 x 5120: 512 rows 88, 58; 1024 rows 89, 93;
+// 2048 rows 176, 144; 8192 rows 440, 533.
+template <int G, bool SF32, bool Z>
+hipError_t launch_shape(const GroupedArgs& g, const W4& w, hipStream_t st) {
+  const long long large = (tiles_of(g, 128, 256) + 255) / 256, small = (tiles_of(g, 64, 128) + 511) / 512;
+  if (56 * small < 100 * large && tile_grid(g, 64, (g.N + 127) / 128) * 256 < (1LL << 32))
+    return launch<Shape<1, 2>, G, SF32, Z>(g, w, st);
+  return launch<Shape<2, 4>, G, SF32, Z>(g, w, st);
 }
 template <int G>
 hipError_t launch_g(const GroupedArgs& g, const W4& w, hipStream_t st) {
-  if (w.scale_f32) return w.zeros ? launch<G, true, true>(g, w, st) : launch<G, true, false>(g, w, st);
-  return w.zeros ? launch<G, false, true>(g, w, st) : launch<G, false, false>(g, w, st);
+  if (w.scale_f32) return w.zeros ? launch_shape<G, true, true>(g, w, st) : launch_shape<G, true, false>(g, w, st);
+  return w.zeros ? launch_shape<G, false, true>(g, w, st) : launch_shape<G, false, false>(g, w, st);
 }
 
 }  // namespace

@@ -131,6 +131,8 @@ SHAPES = [
     ([700], 9, 776), ([4] * 5 + [9, 8, 7], 6, 72), ([300] + [0, 1] * 40, 3, 200), ([0, 1, 2, 3] * 64, 1, 72),
     ([2000, 0, 1, 700, 255, 2500], 5, 328), ([65, 129, 257] * 22, 2, 520), ([4000], 9, 776),
     ([0, 40, 96, 3, 200, 33, 64] * 10, 2, 520), ([300, 31, 600], 1, 16392),
+    ([0, 1, 2500, 700, 130, 2930], 4, 776), ([40] * 30 + [64, 17, 130, 0], 11, 904), ([3, 0, 20], 120, 72),
+    ([1000, 900, 1100, 1024, 960, 1088], 2, 1032),
 ]
 
 
@@ -158,10 +160,11 @@ def test_product(case, group, zeros, sdtype, out_dtype):
 
 @pytest.mark.parametrize("group", [32, 128])
 @pytest.mark.parametrize("zeros", [False, True])
-@pytest.mark.parametrize("counts", [[1, 2, 0, 5], [70, 300, 0, 600]])
-def test_product_exact_on_small_numbers(group, zeros, counts):
+@pytest.mark.parametrize("counts,N", [([1, 2, 0, 5], 264), ([70, 300, 0, 600], 264), ([70, 300, 0, 600], 3080),
+                                      ([700, 3000, 0, 2600], 776)])
+def test_product_exact_on_small_numbers(group, zeros, counts, N):
     """Whole-number rows and power-of-two scales: fp32 sums are exact, so are the results."""
-    g, K, N = gen(5), 640, 264
+    g, K = gen(5), 640
     M = sum(counts)
     a = torch.randint(-8, 9, (M, K), generator=g, device="cuda").to(BF)
     codes, s, z = weights(g, 4, N, K, group, zeros, F32)
@@ -175,11 +178,11 @@ def test_product_exact_on_small_numbers(group, zeros, counts):
         lo += c
 
 
-@pytest.mark.parametrize("per", [1, 3, 20, 300])
+@pytest.mark.parametrize("per,N", [(1, 136), (3, 136), (20, 136), (300, 136), (300, 3080), (2500, 800)])
 @pytest.mark.parametrize("group", [32, 64, 128])
-def test_bad_rows_and_scales_stay_where_they_are(per, group):
+def test_bad_rows_and_scales_stay_where_they_are(per, N, group):
     """An infinity or a NaN in a row reaches that row alone, a NaN scale its column alone; a depth that ends in a stage."""
-    g, E, K, N = gen(3), 3, 384, 136
+    g, E, K = gen(3), 3, 384
     M = E * per
     a = normal(g, M, K)
     codes, s, z = weights(g, E, N, K, group, True, BF)
@@ -202,8 +205,9 @@ def test_bad_rows_and_scales_stay_where_they_are(per, group):
 
 
 @pytest.mark.parametrize("counts", [[7, 0, 28], [900, 0, 1, 400]])
-def test_rows_ahead_of_the_first_expert(counts):
-    g, first, K, N = gen(6), 37, 256, 200
+@pytest.mark.parametrize("N", [200, 2056, 3080])
+def test_rows_ahead_of_the_first_expert(counts, N):
+    g, first, K = gen(6), 37, 256
     a = normal(g, first + sum(counts) + 9, K)
     a[:first], a[first + sum(counts):] = NAN, NAN
     codes, s, z = weights(g, len(counts), N, K, 64, True, BF)
@@ -220,7 +224,7 @@ def test_no_rows():
     moe.moe_w4_dequantize(e(0, 32, t=U8), e(0, 1, t=BF), e(0, 64, t=BF))
 
 
-@pytest.mark.parametrize("counts", [[3, 20], [5, 900]])
+@pytest.mark.parametrize("counts", [[3, 20], [5, 900], [5, 2400], [5, 17995]])
 def test_weights_past_4_gib(counts):
     """The last two of 72 experts of 8192 x 16384."""
     g, E, K, N = gen(22), 72, 8192, 16384
