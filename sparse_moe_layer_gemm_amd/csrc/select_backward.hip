@@ -43,9 +43,29 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectGradArgs a) 
 
   // ---- all scores, where something needs them
   const bool dense = a.dscores || (!a.sigmoid && !a.renorm);
-  float x[N], s[N], m = 0.f, inverse = 0.f;
+  float x[N], s[N], g[N], m = 0.f, inverse = 0.f;
   if (dense) {
     load_logits<CH>(a.logits, a.bf16, t, a.E, i, x);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int e = 64 * c + 4 * i;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) g[4 * c + q] = 0.f;
+      if (a.dscores) {
+        const float* p = a.dscores + (size_t)t * a.E + e;
+        if ((a.E & 3) == 0) {
+          if (e < a.E) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) g[4 * c + q] = v[q];
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (e + q < a.E) g[4 * c + q] = p[q];
+        }
+      }
+    }
     if (!a.sigmoid) {
       float top = x[0];
 #pragma unroll
@@ -54,7 +74,7 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectGradArgs a) 
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        s[j] = x[j] == kNegInf ? 0.f : x[j] == m ? 1.f : expf(x[j] - m);
+        s[j] = x[j] == kNegInf ? 0.f : x[j] == m ? 1.f : exp_neg32(x[j] - m);
         sum += s[j];
       }
       sum = row_sum(sum);
@@ -90,41 +110,22 @@ __global__ __launch_bounds__(256) void select_backward_kernel(SelectGradArgs a) 
     const float v = row_lane<j>(part);
     if ((int)row_lane<j>((uint32_t)id) == id) total += v;
   });
-  __syncthreads();
+  lds_fence();
   if (some) mine[id] = total;
-  __syncthreads();
+  lds_fence();
 
   // ---- every expert's gradient
   f32x4 out[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) out[c] = *reinterpret_cast<const f32x4*>(mine + 64 * c + 4 * i);
   if (dense) {
-    float g[N], sum = 0.f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int e = 64 * c + 4 * i;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) g[4 * c + q] = 0.f;
-      if (a.dscores) {
-        const float* p = a.dscores + (size_t)t * a.E + e;
-        if ((a.E & 3) == 0) {
-          if (e < a.E) {
-            const f32x4 v = *reinterpret_cast<const f32x4*>(p);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) g[4 * c + q] = v[q];
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (e + q < a.E) g[4 * c + q] = p[q];
-        }
-      }
-    }
+    float sum = 0.f;
     if (a.sigmoid) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float e = expf(-fabsf(x[j])), y = 1.f / (1.f + e);
-        if (x[j] != kNegInf) out[j / 4][j & 3] += e * y * y * g[j];
+        // s (1 - s) = e / (1 + e)^2; half steps: 4 by e, 5 by the square's reciprocal, 2 by the products
+        const float e = exp_neg32(-fabsf(x[j])), d = 1.f + e;
+        if (x[j] != kNegInf) out[j / 4][j & 3] += e * __builtin_amdgcn_rcpf(d * d) * g[j];
       }
     } else {
 #pragma unroll
