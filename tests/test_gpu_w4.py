@@ -244,6 +244,22 @@ def test_weights_past_4_gib(counts):
         lo += c
 
 
+@pytest.mark.parametrize("M,N", [(3, 1 << 20), (1 << 22, 8), (70000, 16384)])
+def test_widest_and_tallest(M, N):
+    """2^20 columns; 2^22 rows; grids of more than 2^16 workgroups."""
+    g, K = gen(M), 64
+    codes, s, z = weights(g, 2, N, K, 32, True, BF)
+    a = normal(g, M, K)
+    out = torch.empty(M, N, device="cuda", dtype=BF)
+    moe.moe_w4_grouped_gemm(a, codes, s, ops_ref.offsets_of([M // 3, M - M // 3]), out, zeros=z)
+    for e, (lo, hi) in enumerate(((0, M // 3), (M // 3, M))):
+        rows = torch.arange(lo, hi, device="cuda")
+        rows = rows if M < 100 else torch.cat((rows[:70], rows[-70:]))
+        want = a[rows].double() @ ref.weights64(codes[e], s[e], z[e]).t().contiguous()
+        mag = a[rows].double().abs() @ ref.spread64(codes[e], s[e], z[e]).t().contiguous()
+        close(out[rows], want, ops_ref.sum_bound(want, mag, K + 8, BF))
+
+
 def test_quantise_past_32_bits():
     """More than 2^31 values, by rows and transposed: the last ones."""
     x = torch.zeros(1100, 1024, 2048, dtype=BF, device="cuda")
