@@ -17,8 +17,8 @@
 //
 // The depth is walked in whole stages: behind its end rows are zeros, codes anything
 // finite, and scales 0.
-// Scales and zero points of the tile's columns are fetched 8 groups ahead, 16 bytes of a
-// column at a time, and stand in LDS as fp32, groups apart.
+// Scales s and zero points of the tile's columns are fetched 8 groups ahead, 16 bytes of a
+// column at a time; s and s z stand in LDS as fp32, groups apart.
 #include "w4_common.h"
 
 namespace moe {
@@ -127,54 +127,48 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
     for (int q = 0; q < LB; ++q) dma16(wbuf, woff[q & 1] + ((q >> 1) * 16u * wrow + 128u * s), to + q * 1024);
   };
 
-  // ---- scales (the first half of the wavefronts) and zero points, a column per lane; groups behind the
-  // last count as 0
+  // ---- scales s (the first half of the wavefronts) and products s z (the other half), a column per lane;
+  // groups behind the last count as 0
   const int col = tid & (BN - 1);
   const size_t first = ((size_t)t.e * g.N + min(n0 + col, g.N - 1)) * ng;
   // groups 8 c .. 8 c + 7; the last chunk of a longer row starts early, so that none is read
   // behind the row
   auto chunk_start = [&](int c) { return min(8 * c, ng - 8); };
   u32x4 raw[SF32 ? 2 : 1];
+  u32x2 rawz;
+  const bool upper = tid >= BN;
   auto load_chunk = [&](int c) {
+    if (!Z && upper) return;
     const size_t at = first + chunk_start(c);
-    if (tid < BN) {
-      const uint8_t* p = static_cast<const uint8_t*>(w.scales) + at * (SF32 ? 4 : 2);
+    const uint8_t* p = static_cast<const uint8_t*>(w.scales) + at * (SF32 ? 4 : 2);
 #pragma unroll
-      for (int i = 0; i < (SF32 ? 2 : 1); ++i) raw[i] = reinterpret_cast<const u32x4_any*>(p)[i];
-    } else if constexpr (Z) {
-      const u32x2 d = *reinterpret_cast<const u32x2_any*>(w.zeros + at);
-      raw[0][0] = d[0], raw[0][1] = d[1];
-    }
+    for (int i = 0; i < (SF32 ? 2 : 1); ++i) raw[i] = reinterpret_cast<const u32x4_any*>(p)[i];
+    if (Z && upper) rawz = *reinterpret_cast<const u32x2_any*>(w.zeros + at);
   };
+  float* const chunks = reinterpret_cast<float*>(smem + (upper ? Z0 : S0)) + col;
   auto store_chunk = [&](int c) {
+    if (!Z && upper) return;
     const int shift = 8 * c - chunk_start(c);
-    if (tid < BN) {
-      float* to = reinterpret_cast<float*>(smem + S0 + (c & 1) * CHUNK) + col;
+    float* to = chunks + (c & 1) * (CHUNK / 4);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = SF32 ? __uint_as_float(raw[SF32 ? i >> 2 : 0][i & 3])
-                             : (i & 1) ? bf16_hi(raw[0][(i >> 1) & 3]) : bf16_lo(raw[0][(i >> 1) & 3]);
-        to[((i - shift) & 7) * BN] = i >= shift ? v : 0.f;
-      }
-    } else if constexpr (Z) {
-      float* to = reinterpret_cast<float*>(smem + Z0 + (c & 1) * CHUNK) + col;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        to[((i - shift) & 7) * BN] = i >= shift ? (float)((raw[0][i >> 2] >> (8 * (i & 3))) & 255u) : 0.f;
+    for (int i = 0; i < 8; ++i) {
+      float v = SF32 ? __uint_as_float(raw[SF32 ? i >> 2 : 0][i & 3])
+                     : (i & 1) ? bf16_hi(raw[0][(i >> 1) & 3]) : bf16_lo(raw[0][(i >> 1) & 3]);
+      if (Z && upper) v *= (float)((rawz[i >> 2] >> (8 * (i & 3))) & 255u);
+      to[((i - shift) & 7) * BN] = i >= shift ? v : 0.f;
     }
   };
   auto short_chunk = [&] {  // a row of fewer than 8 groups
-    if (tid < BN) {
-      float* to = reinterpret_cast<float*>(smem + S0) + col;
+    if (!Z && upper) return;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        to[i * BN] = i >= ng ? 0.f
-                     : SF32  ? static_cast<const float*>(w.scales)[first + i]
-                             : bf16_bits_to_f32(static_cast<const uint16_t*>(w.scales)[first + i]);
-    } else if constexpr (Z) {
-      float* to = reinterpret_cast<float*>(smem + Z0) + col;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) to[i * BN] = i < ng ? (float)w.zeros[first + i] : 0.f;
+    for (int i = 0; i < 8; ++i) {
+      float v = 0.f;
+      if (i < ng) {
+        v = SF32 ? static_cast<const float*>(w.scales)[first + i]
+                 : bf16_bits_to_f32(static_cast<const uint16_t*>(w.scales)[first + i]);
+        if (Z && upper) v *= (float)w.zeros[first + i];
+      }
+      chunks[i * BN] = v;
     }
   };
 
@@ -245,29 +239,31 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
         for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(s[j][q], p[i][j][q], acc[i][j][q]);
     keep_here(acc);
   };
-  // less z s t of group n of the stage whose scales are at `at`; -t stands xoff bytes behind xrow
-  auto take_zeros = [&](uint32_t at, auto nn, auto xoff) {
-    constexpr int O = decltype(nn)::value * (BN * 4), X = decltype(xoff)::value;
-    f32x4 s[NJ], z[NJ];
+  // s z t of group n of the stage whose scales are at `at`, taken away: -t (without zero points -8 t) stands
+  // xoff bytes behind xrow, s z (s) beside the scales
+  struct Zeros {
+    f32x4 c[NJ];
     float t[MT];
-    read_scales(s, at, std::integral_constant<int, O>{});
-    if constexpr (Z) read_scales(z, at + (Z0 - S0), std::integral_constant<int, O>{});
+  };
+  auto read_zeros = [&](Zeros& v, uint32_t at, auto nn, auto xoff) {
+    constexpr int O = decltype(nn)::value * (BN * 4), X = decltype(xoff)::value;
+    read_scales(v.c, at + (Z ? Z0 - S0 : 0), std::integral_constant<int, O>{});
 #pragma unroll
-    for (int i = 0; i < MT; ++i) t[i] = __uint_as_float(lds_b32<X>((xrow ^ (64 * i)) + (lds0 + X0)));
-    wait_vec(s);
-    if constexpr (Z) wait_vec(z);
+    for (int i = 0; i < MT; ++i) v.t[i] = __uint_as_float(lds_b32<X>((xrow ^ (64 * i)) + (lds0 + X0)));
+  };
+  auto take_zeros = [&](Zeros& v) {
+    wait_vec(v.c);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(t[i])::"memory");
+    for (int i = 0; i < MT; ++i) asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(v.t[i])::"memory");
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float c = s[j][q] * (Z ? z[j][q] : 8.f);
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i][j][q] = __builtin_fmaf(c, t[i], acc[i][j][q]);
-      }
+        for (int i = 0; i < MT; ++i) acc[i][j][q] = __builtin_fmaf(v.c[j][q], v.t[i], acc[i][j][q]);
     keep_here(acc);
   };
+  auto put_sum = [&](auto off) { lds_put<decltype(off)::value>(xrow + (lds0 + X0), xsum[0] * (Z ? -1.f : -8.f)); };
 
   // ---- start: the first chunk of scales, two stages of codes, three pairs of rows
   if (ng >= 8) load_chunk(0);
@@ -281,7 +277,10 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
   wait_loads<2 * LA + LB>();
   __builtin_amdgcn_s_barrier();
   Step<MT, NJ> f0, f1;
+  f32x4 s0[NJ], s1[NJ];
+  if constexpr (G == 32) read_scales(s0, scale_addr(0), std::integral_constant<int, 0>{});
   read_step(f0, 0, 0, 0, 0);
+  if constexpr (G == 32) wait_vec(s0);
   wait_step(f0);
   int slot = 0;
   for (int ws = 0; ws < nws; ++ws) {
@@ -289,23 +288,28 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
       constexpr int Q = decltype(qq)::value;
       const int pair = 4 * ws + Q;
       const int next = slot == NSA - 1 ? 0 : slot + 1;
-      constexpr bool START0 = G != 128 || (Q & 1) == 0, START1 = false, END1 = G != 128 || (Q & 1) == 1;
+      constexpr bool START0 = G != 128 || (Q & 1) == 0, END1 = G != 128 || (Q & 1) == 1;
       constexpr int FIRST = 64 * Q / G;  // the pair's first group within the stage
-      f32x4 s[NJ];
-      const uint32_t at = scale_addr(ws);
-      constexpr int SECOND = G == 32 ? 1 : 0;
-      constexpr std::integral_constant<int, FIRST * BN * 4> s0{};
-      constexpr std::integral_constant<int, (FIRST + SECOND) * BN * 4> s1{};
-      // step 0, whose fragments are in f0
+      // the pair before: its slot of sums, its first group, whether one ended there
+      constexpr int R = (Q + 3) & 3, N0 = 64 * R / G;
+      constexpr bool ENDED = G != 128 || (R & 1) == 1;
+      const uint32_t at = scale_addr(ws), from = Q == 0 ? scale_addr(max(ws - 1, 0)) : at;
+      constexpr std::integral_constant<int, FIRST * BN * 4> o0{};
+      constexpr std::integral_constant<int, (FIRST + 1) * BN * 4> o1{};
+      Zeros zs;
+      // step 0, whose fragments (and scales, if it is a group) are here; what the next needs is read first
       if constexpr (G == 32) {
-        read_scales(s, at, s0);
-        read_step(f1, slot, 1, ws & 1, 2 * Q + 1);
-        wait_vec(s);
-        mfmas_fold(f0, s);
+        read_scales(s1, at, o1);
+        read_zeros(zs, from, std::integral_constant<int, N0>{}, std::integral_constant<int, R * XS>{});
+      }
+      read_step(f1, slot, 1, ws & 1, 2 * Q + 1);
+      if constexpr (G == 32) {
+        mfmas_fold(f0, s0);
         keep_here(acc);
-        lds_put<Q * XS>(xrow + (lds0 + X0), -xsum[0]);
+        put_sum(std::integral_constant<int, Q * XS>{});
+        take_zeros(zs);
+        wait_vec(s1);
       } else {
-        read_step(f1, slot, 1, ws & 1, 2 * Q + 1);
         mfmas(f0, START0);
       }
       wait_step(f1);
@@ -313,33 +317,36 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
       wait_lds();
       wait_loads<Q == 0 ? LA + LB : LA>();
       __builtin_amdgcn_s_barrier();
-      if constexpr (G == 32) read_scales(s, at, s1);
+      // the large tile has no registers left for what is read before the matrix instructions
+      constexpr bool EARLY = G == 32 || NJ == 2;
+      auto read_ends = [&] {
+        if constexpr (G != 32 && END1) read_scales(s1, at, o0);
+        if constexpr (G == 32)
+          read_zeros(zs, from, std::integral_constant<int, N0 + 1>{}, std::integral_constant<int, R * XS + BM * 4>{});
+        else if constexpr (ENDED)
+          read_zeros(zs, from, std::integral_constant<int, N0>{}, std::integral_constant<int, R * XS>{});
+      };
+      if constexpr (G == 32) read_scales(s0, Q == 3 ? scale_addr(ws + 1) : at, std::integral_constant<int, Q == 3 ? 0 : (FIRST + 2) * BN * 4>{});
+      if constexpr (EARLY) read_ends();
       read_step(f0, next, 0, Q == 3 ? (ws + 1) & 1 : ws & 1, Q == 3 ? 0 : 2 * Q + 2);
       if constexpr (Q == 3) issue_w(ws + 2, ws & 1);
       issue_a(pair + NSA, slot);
       if constexpr (G == 32) {
-        wait_vec(s);
-        mfmas_fold(f1, s);
+        mfmas_fold(f1, s1);
         keep_here(acc);
-        lds_put<Q * XS + BM * 4>(xrow + (lds0 + X0), -xsum[0]);
-        wait_step(f0);
+        put_sum(std::integral_constant<int, Q * XS + BM * 4>{});
+        wait_vec(s0);
       } else {
-        mfmas(f1, START1);
-        if constexpr (END1) read_scales(s, at, s1);
-        wait_step(f0);
-        if constexpr (END1) {
-          wait_vec(s);
-          lds_put<Q * XS>(xrow + (lds0 + X0), -xsum[0]);
-          fold(s);
-        }
+        mfmas(f1, false);
+        if constexpr (!EARLY) read_ends();
       }
-      // zero points of the groups that ended in the pair before (of none, at the start)
-      constexpr int R = (Q + 3) & 3, N0 = 64 * R / G;
-      const uint32_t from = Q == 0 ? scale_addr(max(ws - 1, 0)) : at;
-      if constexpr (G != 128 || (R & 1) == 1)
-        take_zeros(from, std::integral_constant<int, N0>{}, std::integral_constant<int, R * XS>{});
-      if constexpr (G == 32)
-        take_zeros(from, std::integral_constant<int, N0 + 1>{}, std::integral_constant<int, R * XS + BM * 4>{});
+      wait_step(f0);
+      if constexpr (G != 32 && END1) {
+        wait_vec(s1);
+        put_sum(std::integral_constant<int, Q * XS>{});
+        fold(s1);
+      }
+      if constexpr (ENDED) take_zeros(zs);
       // the next 8 groups' scales: loaded behind pair 0, stored behind pair 2 of their last stage but one
       constexpr int SPC = 8 / GPS;  // stages per chunk
       if constexpr (Q == 0) {
@@ -357,9 +364,13 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
   {  // zero points of the last pair's groups
     const uint32_t at = scale_addr(nws - 1);
     constexpr int N0 = 64 * 3 / G;
-    take_zeros(at, std::integral_constant<int, N0>{}, std::integral_constant<int, 3 * XS>{});
-    if constexpr (G == 32)
-      take_zeros(at, std::integral_constant<int, N0 + 1>{}, std::integral_constant<int, 3 * XS + BM * 4>{});
+    Zeros zs;
+    read_zeros(zs, at, std::integral_constant<int, N0>{}, std::integral_constant<int, 3 * XS>{});
+    take_zeros(zs);
+    if constexpr (G == 32) {
+      read_zeros(zs, at, std::integral_constant<int, N0 + 1>{}, std::integral_constant<int, 3 * XS + BM * 4>{});
+      take_zeros(zs);
+    }
   }
 
   // ---- epilogue: lane l holds row l % 16 of a tile, columns 16 j + 4 (l / 16) + 0..3.
