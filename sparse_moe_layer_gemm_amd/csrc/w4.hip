@@ -5,10 +5,12 @@
 // A group of G values along K has the scale s = max|v| * (1/7), codes
 // rn(v / s) + 8; with zero points s = (max(v, 0) - min(v, 0)) * (1/15), z = rn(-min / s),
 // codes rn(v / s) + z; rn: to the nearest whole number, of two equally near ones the
-// even one, of the exact quotient. bf16 values under a bf16 scale often lie half way
-// between two codes, so the quotient has to be exact there: q = rn(v * (1 / s)) is
-// off by one step at most, and only where |v - q s|, which one FMA gives exactly,
-// reaches s / 2.
+// even one, of the exact quotient. Quotients often lie half way between two codes (bf16
+// values under a bf16 scale do), so they have to be exact there. In general q = rn(v * (1 / s))
+// is off by one step at most, and only where |v - q s|, which one FMA gives exactly, reaches
+// s / 2. bf16 values under a bf16 scale need less: with mantissas of 8 bits V and S a quotient
+// near m / 2 is off it by a multiple of 1 / (4 S), 2^-10 at least, or not at all, so that v * (1 / s)
+// rounded to multiples of 2^-10 tells both apart, and is then rounded to a whole number.
 #include "ops_common.h"
 #include "w4_internal.h"
 
@@ -75,19 +77,27 @@ __device__ __forceinline__ Group make_group(const Range& r) {
   g.s = s;
   g.ok = finite && s > 0.f;
   g.up = s < 0x1p-90f ? 0x1p64f : 1.f;
-  g.inverse = g.ok ? 1.f / (s * g.up) : 0.f;
+  g.inverse = g.ok ? __builtin_amdgcn_rcpf(s * g.up) : 0.f;
   g.zero = Z ? 0.f : 8.f;
   if (Z && g.ok) g.zero = fminf(fmaxf(nearest(-r.lo * g.up, s * g.up, g.inverse), 0.f), 15.f);
   return g;
 }
-// Codes of 8 values (element 2j in the low nibble of byte j).
+// Codes of 8 values (element 2j in the low nibble of byte j). SHORT: values and scale are bf16 numbers.
+template <bool SHORT>
 __device__ __forceinline__ uint32_t codes8(const float* v, const Group& g) {
   uint32_t d = 0;
   const float s = g.s * g.up;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    float q = g.zero;
-    if (g.ok) q = fminf(fmaxf(nearest(v[j] * g.up, s, g.inverse) + g.zero, 0.f), 15.f);
+    const float x = v[j] * g.up;
+    float q;
+    if constexpr (SHORT) {
+      const float t = __builtin_fmaf(x, g.inverse, 0x1.8p13f);  // whole multiples of 2^-10
+      q = (t + (0x1.8p23f - 0x1.8p13f)) - 0x1.8p23f;            // whole numbers, ties to even
+    } else {
+      q = nearest(x, s, g.inverse);
+    }
+    q = g.ok ? fminf(fmaxf(q + g.zero, 0.f), 15.f) : g.zero;
     d |= (uint32_t)q << (4 * j);
   }
   return d;
@@ -129,7 +139,7 @@ __global__ __launch_bounds__(256) void w4_quantize_rows_kernel(const void* __res
   if (group >= 64) join_lanes<Z, 0x141>(r);   // the other quad of 8
   if (group >= 128) join_lanes<Z, 0x140>(r);  // the other half of 16
   const Group g = make_group<Z, SF32>(r);
-  codes[i] = codes8(v, g);
+  codes[i] = codes8<BF16 && !SF32>(v, g);
   const int lanes = group >> 3;
   if ((threadIdx.x & (lanes - 1)) == 0) store_group<Z, SF32>(g, i / lanes, scales, zeros);
 }
@@ -192,7 +202,7 @@ __global__ __launch_bounds__(512) void w4_quantize_cols_kernel(const void* __res
         float v[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) v[r] = value(8 * j + r, h);
-        q[j] = codes8(v, g);
+        q[j] = codes8<BF16 && !SF32>(v, g);
       }
       const int lc = CPL * lane + h;
       *reinterpret_cast<u32x4*>(tile + lc * 128 + ((wave ^ (lane & 7)) << 4)) = q;

@@ -87,6 +87,23 @@ def test_quantise_every_tie(zeros, sdtype):
     assert torch.equal(check_quantise(x.contiguous(), group, zeros, sdtype)[1].float(), s)
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("power", [0, -100, -126, 100])
+def test_quantise_every_bf16(zeros, power):
+    """All mantissas of bf16 values under all mantissas of bf16 scales, over the exponents of quotients 1/32 .. 16."""
+    m = torch.arange(128, 256, device="cuda").double()
+    values = torch.cat([m * 2.0 ** e for e in range(-9, 1)])
+    values = torch.cat((values, -values, torch.zeros(10 * 127 * 3 - 2560, dtype=torch.float64, device="cuda")))
+    top = m * (1.0 if zeros else 0.5)
+    top = torch.cat((top, top * 2))
+    x = torch.zeros(len(top), 30, 128, dtype=torch.float64, device="cuda")
+    x[:, :, :127] = values.view(30, 127).clamp(min=-m.max() * (0.0 if zeros else 1.0))
+    x = torch.minimum(torch.maximum(x, -top[:, None, None]), top[:, None, None])
+    x[:, :, 127] = top[:, None]
+    x = (x * 2.0 ** (power - 7)).to(BF).view(len(top), 30 * 128)
+    check_quantise(x, 128, zeros, BF)
+
+
 def weights(g, E, N, K, group, zeros, sdtype):
     """Codes of every value, scales and zero points (bytes of all sizes among them), between guards."""
     codes, _ = ops_ref.guarded(torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda").to(U8), 16, 0xFF)
