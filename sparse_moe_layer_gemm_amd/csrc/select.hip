@@ -23,9 +23,14 @@
 //    them where one of its tokens is not certain, about one in a hundred.
 // Weights and scores are formed alike on both ways.
 //
-// Groups: the choices cross through LDS, one slot left free per group so that lanes that
+// Groups: the choices cross through LDS, slots left free after each group so that lanes that
 // walk neighbouring groups meet different banks; several lanes share a group while there
 // are 8 at most.
+//
+// Bound by vector instructions, about 1200 for four tokens of 160 experts with bias and
+// groups. Measured: 131072 tokens x 160 experts, 6 chosen from 3 of 8 groups with a bias,
+// all scores written: 80 us (2.2 TB/s; 107 with fp64 keys alone; without bias and groups 36);
+// 128 tokens x 256 experts, 8 from 4 of 8 groups: 7.0 us.
 #include "select_common.h"
 #include "select_internal.h"
 

@@ -11,6 +11,9 @@
 // s / 2. bf16 values under a bf16 scale need less: with mantissas of 8 bits V and S a quotient
 // near m / 2 is off it by a multiple of 1 / (4 S), 2^-10 at least, or not at all, so that v * (1 / s)
 // rounded to multiples of 2^-10 tells both apart, and is then rounded to a whole number.
+//
+// Bound by HBM: 32 x 5120 x 1536 transposed 131 us (4.9 TB/s), and back 86 us (7.3 TB/s, past
+// the caches); 1536 x 5120 by rows 7.4 us.
 #include "ops_common.h"
 #include "w4_internal.h"
 

@@ -17,6 +17,12 @@
 //
 // The depth is walked in whole stages: behind its end rows are zeros, codes anything
 // finite, and scales 0.
+//
+// Bound by the issue of instructions: per 256 of depth a wavefront of the large tile has 637
+// vector instructions (2550 cycles) beside 136 MFMAs (2180 cycles), and they hardly overlap.
+// 32768 rows over 64 experts, 5120 x 2560, G = 128: 1016 us, 846 TFLOP/s (without its loads
+// 983, without the group sums 905, MFMAs alone 695); 1998 rows over 48 experts, 1440 x 2056,
+// G = 32 with zero points: 67 us on the small tile.
 // Scales s and zero points of the tile's columns are fetched 8 groups ahead, 16 bytes of a
 // column at a time; s and s z stand in LDS as fp32, groups apart.
 #include "w4_common.h"
