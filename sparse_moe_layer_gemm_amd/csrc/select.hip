@@ -20,7 +20,8 @@
 //    the next are D (a logit's: 1) units apart.
 //  - 64-bit keys, as fp64 numbers (of which a maximum or minimum is one instruction, too):
 //    the logit, or score + bias formed in fp64 and kept to 44 bits. A wavefront takes
-//    them where one of its tokens is not certain, about one in a hundred.
+//    them where one of its tokens is not certain: about one in a hundred, and all whose
+//    largest choice a bias takes past 4 in magnitude.
 // Weights and scores are formed alike on both ways.
 //
 // Groups: the choices cross through LDS, slots left free after each group so that lanes that

@@ -465,8 +465,7 @@ long long tiles_of(const GroupedArgs& g, int bm, int bn) {
 template <int G, bool SF32, bool Z>
 hipError_t launch_shape(const GroupedArgs& g, const W4& w, hipStream_t st) {
   const long long large = (tiles_of(g, 128, 256) + 255) / 256, small = (tiles_of(g, 64, 128) + 511) / 512;
-  if (56 * small < 100 * large && tile_grid(g, 64, (g.N + 127) / 128) * 256 < (1LL << 32))
-    return launch<Shape<1, 2>, G, SF32, Z>(g, w, st);
+  if (56 * small < 100 * large) return launch<Shape<1, 2>, G, SF32, Z>(g, w, st);
   return launch<Shape<2, 4>, G, SF32, Z>(g, w, st);
 }
 template <int G>

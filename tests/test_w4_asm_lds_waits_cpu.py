@@ -1,6 +1,6 @@
 """The products with 4-bit integer weights read LDS with inline-asm instructions and explicit waits: on their gfx950
 ISA, no instruction touches such a destination before a wait that covers its read, on any control-flow path (the
-checker and its planted mistake: test_asm_lds_waits_cpu.py), and nothing spills."""
+check and its planted mistake: test_asm_lds_waits_cpu.py), and nothing spills."""
 import os
 import subprocess
 
