@@ -411,11 +411,12 @@ moe_status moe_mxfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scale
  * arithmetic orders them (with a bias by 44 bits of them), whatever type is used on the way.
  * Scores are fp32 results (a sigmoid within 10 half steps, a softmax within 36 and what the
  * rounding of logit - maximum makes of an exponential); the weights are formed from the
- * chosen logits in fp64 and rounded once (softmax without renorm: with the fp32 sum of all). An expert whose logit is NaN or -infinity is left out: its score is
- * 0, it is never chosen. Nor is one whose bias is NaN or -infinity. Slots for which
- * no expert is left get id -1 and weight 0: moe_permute leaves such pairs without a
- * row and the finalize calls add nothing for them. A logit of +infinity is the limit
- * of large ones (several share the softmax evenly).
+ * chosen logits in fp64 and rounded once (softmax without renorm: with the fp32 sum of
+ * all). An expert whose logit is NaN or -infinity is left out: its score is 0, it is never
+ * chosen. Nor is one whose bias is NaN or -infinity. Slots for which no expert is left get
+ * id -1 and weight 0: moe_permute leaves such pairs without a row and the finalize calls
+ * add nothing for them. A logit of +infinity is the limit of large ones (several share
+ * the softmax evenly).
  *   topk_ids [T, k] int32; topk_w [T, k] f32; scores [T, E] f32, or NULL
  * 1 <= k <= 8, k <= E <= 256, groups (1: none) divides E, is at most 64 and
  * 1 <= group_k <= groups with k <= group_k * E / groups; scale finite;

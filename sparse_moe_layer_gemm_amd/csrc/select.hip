@@ -14,14 +14,14 @@
 //    choice below the token's largest: the logit, 2^-19 a unit, or score + bias in fp32,
 //    2^-23 a unit. A logit's units never order two logits wrongly (they only fall together),
 //    and a choice's are off by less than D / 2: a sigmoid score (of 1 at most) by 5, its sum
-//    with the bias (of 6 in magnitude at most) by 2, the difference, its product and the
-//    cut by 3: D = 24; a softmax score by 18, with a sum of 256 terms and the
-//    exponentials' arguments: D = 64. So the order is certain where the chosen ones and
+//    with the bias, of 2 more than the largest choice's magnitude c at most, by c / 2 + 1, the
+//    difference, its product and the cut by 3: D = 24 + 2 c; a softmax score by 18, with a sum
+//    of 256 terms and the exponentials' arguments: D = 64 + 2 c. So the order is certain where the chosen ones and
 //    the next are D (a logit's: 1) units apart.
 //  - 64-bit keys, as fp64 numbers (of which a maximum or minimum is one instruction, too):
 //    the logit, or score + bias formed in fp64 and kept to 44 bits. A wavefront takes
-//    them where one of its tokens is not certain: about one in a hundred, and all whose
-//    largest choice a bias takes past 4 in magnitude.
+//    them where one of its tokens is not certain, about one in a hundred, or whose largest
+//    choice a bias takes past 1000 in magnitude.
 // Weights and scores are formed alike on both ways.
 //
 // Groups: the choices cross through LDS, slots left free after each group so that lanes that
@@ -138,7 +138,7 @@ __device__ __forceinline__ int group_of(const SelectArgs& a, int e) { return (e 
 // unsure: whether two groups are too close to tell.
 template <bool BIASED, int N>
 __device__ __forceinline__ uint64_t kept_groups32(const SelectArgs& a, const float (&c)[N], float* lds, int i,
-                                                  float m, bool& unsure) {
+                                                  float high, bool& unsure) {
   float* counts = lds;
   lds += (a.groups + 3) & ~3;
   const bool fours = (a.group_size & 3) == 0;  // four at a time, groups 4 slots apart
@@ -183,7 +183,7 @@ __device__ __forceinline__ uint64_t kept_groups32(const SelectArgs& a, const flo
     if (share >= 3) join(row_get<ROW_HALF_MIRROR>(one), row_get<ROW_HALF_MIRROR>(two));
     float value = one;
     if (a.group_top == 2 && one != kNegInf) {
-      auto part = [&](float l) { return BIASED ? l : a.sigmoid ? sigmoid32(l) : exp_neg32(l - m); };
+      auto part = [&](float l) { return BIASED ? l : a.sigmoid ? sigmoid32(l) : exp_neg32(l - high); };
       value = part(one) + (two == kNegInf ? 0.f : part(two));
     }
     if (g < a.groups) counts[g] = value;
@@ -196,8 +196,9 @@ __device__ __forceinline__ uint64_t kept_groups32(const SelectArgs& a, const flo
     if (g < a.groups && counts[g] != kNegInf) {
       ahead = 0;
       const float mine = counts[g];
-      // twice the error of a group's two scores (16 units of 2^-23 each), and roundings of large sums
-      const float near = exact ? -1.f : 0x1p-17f + 0x1p-21f * fabsf(mine);
+      // Twice the error of a group's two scores (16 units of 2^-23 each) and the roundings of their sums with the
+      // bias, whose magnitudes together are no more than the group's and twice the largest choice's.
+      const float near = exact ? -1.f : 0x1p-17f + 0x1p-21f * (fabsf(mine) + (BIASED ? fabsf(high) : 0.f));
       for (int h = 0; h < a.groups; ++h) {
         const float other = counts[h];
         ahead += other > mine || (other == mine && h < g);
@@ -388,7 +389,6 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a) {
 
   // ---- choices in fp32, the groups that stay, 32-bit keys
   const bool exact = !BIASED && a.bf16;
-  const int D = BIASED ? (a.sigmoid ? 24 : 64) : 1;
   bool unsure = false;
   float c[N];
 #pragma unroll
@@ -401,7 +401,8 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a) {
     for (int j = 0; j < N; ++j) c[j] = x[j] == kNegInf ? kNegInf : s[j] + b[j];
     high = row_top1(c);
   }
-  if ((!exact || a.group_top == 2) && high != kNegInf && !(fabsf(high) <= (BIASED ? 4.f : 0x1p120f))) unsure = true;
+  if ((!exact || a.group_top == 2) && high != kNegInf && !(fabsf(high) <= (BIASED ? 1000.f : 0x1p120f))) unsure = true;
+  const int D = BIASED ? (a.sigmoid ? 24 : 64) + (int)(2.f * fminf(fabsf(high), 1000.f)) : 1;
   uint32_t v[N];
   const uint32_t least = exact ? 0x00800000u : 256u;  // keys below stand for none
   if (exact) {
@@ -418,7 +419,7 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a) {
     }
   }
   if (a.groups > 1)
-    drop_groups(a, kept_groups32<BIASED>(a, c, reinterpret_cast<float*>(own), i, m, unsure), i, v, 0u);
+    drop_groups(a, kept_groups32<BIASED>(a, c, reinterpret_cast<float*>(own), i, high, unsure), i, v, 0u);
   uint32_t top[KT], mine = 0;
   row_top<KT>(v, 0u, top);
 #pragma unroll

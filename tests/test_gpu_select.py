@@ -165,6 +165,23 @@ def test_select_backward(shape, score, renorm, dtype, dl_dtype, dense):
     assert torch.equal(again, dl)
 
 
+@pytest.mark.parametrize("level", [-2000.0, -300.0, -20.0, 5.0, 20.0, 300.0, 900.0, 1e5])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [dict(), dict(groups=8, group_k=3, group_top=2), dict(groups=8, group_k=3)])
+def test_bias_of_any_level(level, score, groups):
+    """A common level in the bias costs the choices their last bits in fp32: they are ordered as in fp64, some of them
+    a few fp32 steps of that level apart, and so are groups whose largest choices cancel."""
+    T, E, k = 48, 64, 6
+    g = gen(int(abs(level)))
+    l = torch.randn(T, E, generator=g, device="cuda")
+    l[::2] = l[::2, :1] + torch.randn(T // 2, E, generator=g, device="cuda") * abs(level) * 2.0 ** -23
+    bias = level + torch.randn(E, generator=g, device="cuda") * 0.1
+    bias[::4] = level
+    check(l, k, score=score, renorm=True, bias=bias, **groups)
+    bias[::8] = -level
+    check(l, k, score=score, renorm=True, bias=bias, **groups)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_gradient_against_differences(score, renorm):
