@@ -19,7 +19,9 @@ SOURCES = ["abi.cpp", "router.hip", "permute.hip", "expert_stream.hip", "expert_
            "finalize.hip",
            "finalize_norm.hip", "hbm_read.hip", "noalloc.hip", "abi_ops.cpp", "grouped_simple.hip", "grouped_tile.hip", "grouped_stream.hip",
            "mxfp4_tile.hip",
-           "swiglu.hip", "finalize_backward.hip", "mxfp4.hip", "abi_select.cpp", "select.hip", "select_backward.hip", "abi_w4.cpp", "w4.hip", "w4_stream.hip", "w4_tile.hip"]
+           "swiglu.hip", "finalize_backward.hip", "mxfp4.hip",
+           "abi_select.cpp", "select.hip", "select_backward.hip",
+           "abi_w4.cpp", "w4.hip", "w4_stream.hip", "w4_tile.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
