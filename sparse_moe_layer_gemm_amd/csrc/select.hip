@@ -134,8 +134,8 @@ __device__ __forceinline__ int expert_of(int i, int j) { return 64 * (j >> 2) + 
 __device__ __forceinline__ int group_of(const SelectArgs& a, int e) { return (e * a.group_magic) >> 16; }
 
 // ---- groups. c: the lane's choices (-infinity: may not be chosen); lds: this token's: the groups'
-// counts, then the choices of all 64 CH experts there might be. Returns bit g for a group that stays, the same in the row's lanes;
-// unsure: whether two groups are too close to tell.
+// counts, then the choices of all 64 CH experts there might be; high: the largest choice. Returns bit g for a
+// group that stays, the same in the row's lanes; unsure: whether two groups are too close to tell.
 template <bool BIASED, int N>
 __device__ __forceinline__ uint64_t kept_groups32(const SelectArgs& a, const float (&c)[N], float* lds, int i,
                                                   float high, bool& unsure) {
@@ -146,7 +146,8 @@ __device__ __forceinline__ uint64_t kept_groups32(const SelectArgs& a, const flo
   for (int c4 = 0; c4 < N / 4; ++c4) {
     const int e = expert_of(i, 4 * c4);
     if (fours) {
-      *reinterpret_cast<f32x4*>(lds + e + 4 * group_of(a, e)) = f32x4{c[4 * c4], c[4 * c4 + 1], c[4 * c4 + 2], c[4 * c4 + 3]};
+      *reinterpret_cast<f32x4*>(lds + e + 4 * group_of(a, e)) =
+          f32x4{c[4 * c4], c[4 * c4 + 1], c[4 * c4 + 2], c[4 * c4 + 3]};
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q) lds[e + q + group_of(a, e + q)] = c[4 * c4 + q];

@@ -332,7 +332,10 @@ __device__ __forceinline__ void tile_body(const GroupedArgs& g, const W4& w, uin
         else if constexpr (ENDED)
           read_zeros(zs, from, std::integral_constant<int, N0>{}, std::integral_constant<int, R * XS>{});
       };
-      if constexpr (G == 32) read_scales(s0, Q == 3 ? scale_addr(ws + 1) : at, std::integral_constant<int, Q == 3 ? 0 : (FIRST + 2) * BN * 4>{});
+      if constexpr (G == 32) {
+        constexpr std::integral_constant<int, Q == 3 ? 0 : (FIRST + 2) * BN * 4> o2{};
+        read_scales(s0, Q == 3 ? scale_addr(ws + 1) : at, o2);
+      }
       if constexpr (EARLY) read_ends();
       read_step(f0, next, 0, Q == 3 ? (ws + 1) & 1 : ws & 1, Q == 3 ? 0 : 2 * Q + 2);
       if constexpr (Q == 3) issue_w(ws + 2, ws & 1);
