@@ -285,9 +285,9 @@ hipError_t launch_g(const GroupedArgs& g, const W4& w, hipStream_t st) {
 }  // namespace
 
 // The streaming kernel or tiles? Measured at 5120 x 1536 (one expert: 5120 x 5120), G = 128, us, streaming
-// against the faster tiles, by experts x rows: 1 x 16 14, 32; 1 x 128 28, 47; 1 x 256 41, 47; 1 x 512 70, 58;
-// 16 x 32 34, 48; 16 x 64 57, 60; 16 x 128 90, 61; 64 x 16 80, 97; 64 x 32 112, 110; 64 x 64 179, 148;
-// 256 x 16 276, 301; 256 x 32 405, 351; 48 x 42 at 1440 x 2056, G = 32: 94, 75. So: below 32 rows per expert, and
+// against the faster tiles, by experts x rows: 1 x 16 14, 32; 1 x 128 28, 47; 1 x 256 41, 47; 1 x 512 70, 56;
+// 16 x 32 34, 48; 16 x 64 57, 60; 16 x 128 90, 62; 64 x 16 80, 97; 64 x 32 112, 106; 64 x 64 179, 143;
+// 256 x 16 276, 301; 256 x 32 405, 347; 48 x 42 at 1440 x 2056, G = 32: 94, 71. So: below 32 rows per expert, and
 // where the tiles are too few for the CUs; if the scales of 64 columns fit in LDS, and the grid in a launch.
 bool w4_prefer_stream(const GroupedArgs& g, const W4& w) {
   if (table_bytes(g, w) > 64 * 1024 || tile_grid(g, 8, (g.N + BN - 1) / BN) * 256 >= (1LL << 32)) return false;

@@ -462,9 +462,9 @@ long long tiles_of(const GroupedArgs& g, int bm, int bn) {
 }
 // Which tile? 512 small ones take 0.56 of 256 large ones' time where both fill the CUs, so the
 // shape with fewer rounds at those weights. Measured at 5120 x 1536, G = 128, us, large against
-// small, experts x rows: 64 x 64 181, 148; 64 x 128 267, 220; 64 x 256 357, 375; 64 x 512 619, 696;
-// 256 x 128 830, 813; 16 x 128 92, 61; one expert, 5120 x 5120: 512 rows 88, 58; 1024 rows 89, 93;
-// 2048 rows 176, 144; 8192 rows 440, 533.
+// small, experts x rows: 64 x 64 180, 143; 64 x 128 265, 216; 64 x 256 356, 372; 64 x 512 620, 698;
+// 256 x 128 822, 810; 16 x 128 92, 62; one expert, 5120 x 5120: 512 rows 87, 56; 1024 rows 88, 89;
+// 2048 rows 175, 142; 8192 rows 446, 536.
 template <int G, bool SF32, bool Z>
 hipError_t launch_shape(const GroupedArgs& g, const W4& w, hipStream_t st) {
   const long long large = (tiles_of(g, 128, 256) + 255) / 256, small = (tiles_of(g, 64, 128) + 511) / 512;
