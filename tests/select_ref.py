@@ -117,3 +117,49 @@ def backward(logits, ids, dw, score="softmax", renorm=True, scale=1.0, dscores=N
         out.append([p + d for p, d in zip(part, dense)])
         bound.append([e + 10 * u * m + u * abs(p + d) + 1e-37 for e, m, p, d in zip(err, mag, part, dense)])
     return torch.tensor(out, dtype=torch.float64).view(T, E), torch.tensor(bound, dtype=torch.float64).view(T, E)
+
+
+def backward_sure(logits, ids, dw, score, renorm, scale, dscores=None):
+    """(d logits, a bound of their error) as backward's, by sums over pairs of experts: d - sum d r is sum_i r_i (d_j - d_i), which
+    loses nothing where one expert has nearly all of the sum. Rows without infinities, ids that differ.
+
+    The bound counts fp32 roundings, u = 2^-24. Softmax: s is off by |x - m| + 36, the moved h (h less that of the expert that
+    has more than half, formed from the parts of both) by 3, its products with s, their sum and the last difference and product
+    by 26: K = |x - m| + 50 for every s, of what is moved. What the slots give besides: 1 of itself, and fp64 roundings."""
+    u = 2.0 ** -24
+    T, E = logits.shape
+    out, bound = [], []
+    for t, row in enumerate(logits.double().tolist()):
+        s = scores_of(row, score)
+        slots = list(zip(ids[t].tolist(), dw[t].double().tolist()))
+        g = dscores[t].double().tolist() if dscores is not None else [0.0] * E
+        dl, err, D = [0.0] * E, [0.0] * E, [0.0] * E
+        if score == "softmax" and not renorm:
+            for e, d in slots:
+                D[e] = scale * d
+        else:
+            r = scores_of([row[e] for e, _ in slots], "softmax") if score == "softmax" else [s[e] for e, _ in slots]
+            total = math.fsum(r) if renorm else 1.0
+            r = [x / total for x in r]
+            for (e, d), x in zip(slots, r):
+                w = scale * x * (_one_minus_sig(row[e]) if score == "sigmoid" else 1.0)
+                terms = [y * (d - c) for (_, c), y in zip(slots, r)] if renorm else [d]
+                dl[e] = w * math.fsum(terms)
+                err[e] = 1.01 * u * abs(dl[e]) + 2.0 ** -44 * abs(w) * sum(abs(v) for v in terms)
+        if score == "sigmoid":
+            for e in range(E):
+                v = s[e] * _one_minus_sig(row[e]) * g[e]
+                err[e] += 12 * u * abs(v) + u * abs(dl[e] + v)
+                dl[e] += v
+        elif dscores is not None or not renorm:
+            most = max(range(E), key=lambda e: s[e])
+            d0, g0 = (D[most], g[most]) if s[most] > 0.5 else (0.0, 0.0)
+            H = [abs(D[e] - d0) + abs(g[e] - g0) for e in range(E)]
+            K = [max(row) - x + 50 for x in row]
+            for e in range(E):
+                v = s[e] * math.fsum(s[f] * ((D[e] - D[f]) + (g[e] - g[f])) for f in range(E))
+                err[e] += u * s[e] * (K[e] * H[e] + math.fsum(s[f] * H[f] * (K[e] + K[f]) for f in range(E))) + u * abs(dl[e] + v)
+                dl[e] += v
+        out.append(dl)
+        bound.append([x + 1e-37 for x in err])
+    return torch.tensor(out, dtype=torch.float64).view(T, E), torch.tensor(bound, dtype=torch.float64).view(T, E)

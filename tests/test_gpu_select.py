@@ -1,4 +1,6 @@
 """Routing by scores and its gradient on the GPU against plain 64-bit forms."""
+import math
+
 import pytest
 import torch
 
@@ -281,3 +283,36 @@ def test_streams_and_graphs():
         both(ls[1], eager)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(o, w)) and torch.equal(eager[1], want[1][1])
+
+
+@pytest.mark.parametrize("E,k,first", [(2, 1, 0), (2, 1, 1), (7, 3, 0), (64, 1, 0), (64, 8, 1), (200, 8, 0), (256, 2, 0)])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+@pytest.mark.parametrize("dense", [False, True])
+def test_gradient_of_sure_tokens(E, k, first, score, renorm, dense):
+    """Tokens whose largest score is nearly all of the sum: the gradients are its small rest, to the digits that the rest
+    has. first 0: the largest is the first slot, 1: it is not among the slots (k = 1) or is the second."""
+    gaps = torch.tensor([8.0, 12.0, 16.0, 17.0, 20.0, 25.0, 33.0, 40.0, 60.0], device="cuda").repeat(2)
+    T, g = len(gaps), gen(E + k)
+    l = torch.randn(T, E, generator=g, device="cuda") * 0.5
+    top = torch.randint(0, E, (T,), generator=g, device="cuda")
+    at = torch.arange(T, device="cuda")
+    # by gap over all others' sum
+    l[at, top] = gaps + l.amax(1) + math.log(E)
+    if score == "sigmoid":  # scores far below 1 are in the ratios of a softmax
+        l -= l.amax(1, keepdim=True) + 1
+    others = torch.rand(T, E, generator=g, device="cuda")
+    others[at, top] = 2.0
+    order = others.argsort(1, descending=True)
+    if first:
+        order = torch.cat((order[:, 1:2], order[:, :1], order[:, 2:]), 1)
+    ids = order[:, :k].to(torch.int32).contiguous()
+    dw = torch.randn(T, k, generator=g, device="cuda")
+    dw[T // 2:] = 1 + dw[T // 2:] * 2.0 ** -12  # nearly equal ones
+    ds = torch.randn(T, E, generator=g, device="cuda") * 0.1 if dense else None
+    for dl_dtype in (F32, BF):
+        dl = torch.empty(T, E, device="cuda", dtype=dl_dtype)
+        moe.moe_select_backward(l, ids, dw, dl, score=score, renorm=renorm, scale=2.5, dscores=ds)
+        want, bound = ref.backward_sure(l.cpu(), ids.cpu(), dw.cpu(), score, renorm, 2.5, None if ds is None else ds.cpu())
+        err = (dl.cpu().double() - want).abs()
+        bound = bound + ops_ref.HALF[dl_dtype] * (want.abs() + bound)
+        assert bool((err <= bound).all()), (err / bound).max()

@@ -119,3 +119,20 @@ def test_plain_gradient_is_that_of_the_plain_form(score, renorm):
             a[t, e] += h
             b[t, e] -= h
             assert abs((loss(a) - loss(b)) / (2 * h) - got[t, e].item()) < 1e-8
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+def test_gradient_by_pairs_is_the_formula(score, renorm):
+    """The sums over pairs of experts against the formula, in 64 bits, and what they keep where the formula loses it."""
+    g = torch.Generator().manual_seed(8)
+    l, ds = torch.randn(5, 9, generator=g), torch.randn(5, 9, generator=g)
+    dw, ids = torch.randn(5, 4, generator=g), torch.rand(5, 9, generator=g).argsort(1)[:, :4].to(torch.int32)
+    for d in (None, ds):
+        a, b = (f(l, ids, dw, score, renorm, 1.5, d)[0] for f in (ref.backward, ref.backward_sure))
+        assert (a - b).abs().max() < 1e-13
+    # two experts 50 apart, the surer one chosen: s (1 - s) d, 1 - s = 1 / (1 + e^50)
+    l = torch.tensor([[50.0, 0.0]])
+    got, bound = ref.backward_sure(l, torch.tensor([[0]]), torch.tensor([[3.0]]), "softmax", False, 1.0)
+    want = 3 / (1 + math.exp(50.0)) * (1 / (1 + math.exp(-50.0)))
+    assert abs(got[0, 0].item() / want - 1) < 1e-14 and abs(got[0, 1].item() / want + 1) < 1e-14
+    assert (bound < 2e-5 * want).all()
