@@ -34,6 +34,7 @@
 // 128 tokens x 256 experts, 8 from 4 of 8 groups: 7.0 us.
 #include "select_common.h"
 #include "select_internal.h"
+#include "select_keys.h"
 
 namespace moe {
 namespace {
@@ -414,9 +415,7 @@ __global__ __launch_bounds__(256) void select_kernel(SelectArgs a) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const float units = __builtin_fmaf(c[j] - high, BIASED ? 0x1p23f : 0x1p19f, 0x1p24f - 1.f);
-      // 1 at least, but 0 for -infinity: the middle one of units, 1 and a large number (-infinity there)
-      const float clamped = __builtin_amdgcn_fmed3f(units, 1.f, __builtin_fmaf(c[j], 0x1p-30f, 0x1p100f));
-      v[j] = (uint32_t)clamped << 8 | (uint32_t)(255 - expert_of(i, j));
+      v[j] = choice_key(c[j], units, expert_of(i, j));
     }
   }
   if (a.groups > 1)

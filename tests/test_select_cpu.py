@@ -1,10 +1,12 @@
 """Routing by scores on the host: the plain form against hand-made rows, and every refusal before anything is enqueued."""
 import math
+import subprocess
 
 import pytest
 import torch
 
 import sparse_moe_layer_gemm_amd as moe
+from sparse_moe_layer_gemm_amd import build as pkg_build
 from tests import select_ref as ref
 
 OK, INVAL, UNSUP = 0, 1, 2
@@ -136,3 +138,30 @@ def test_gradient_by_pairs_is_the_formula(score, renorm):
     want = 3 / (1 + math.exp(50.0)) * (1 / (1 + math.exp(-50.0)))
     assert abs(got[0, 0].item() / want - 1) < 1e-14 and abs(got[0, 1].item() / want + 1) < 1e-14
     assert (bound < 2e-5 * want).all()
+
+
+def test_keys_convert_nothing_out_of_range(tmp_path):
+    """The 32-bit keys' conversion to whole numbers, built with a check of its range: experts that are left out, rows of
+    them, infinite choices (whose distance to the largest is NaN), choices far below the largest."""
+    src, exe = tmp_path / "keys.cpp", tmp_path / "keys"
+    src.write_text("""
+#include <math.h>
+#include <stdio.h>
+#include "select_keys.h"
+int main() {
+  const float inf = INFINITY, rows[][2] = {{-inf, 0.f}, {-inf, -inf}, {-inf, inf}, {inf, inf}, {0.f, inf}, {-3e38f, 3e38f},
+                                           {-40.f, 0.f}, {1.f, 1.f}, {0.75f, 1.f}, {-1e-40f, 0.f}};
+  for (const auto& r : rows) {
+    volatile float c = r[0], high = r[1];
+    printf("%u ", moe::choice_key(c, fmaf(c - high, 0x1p19f, 0x1p24f - 1.f), 5));
+  }
+}
+""")
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-I", pkg_build.CSRC, "-fsanitize=float-cast-overflow",
+                        "-fno-sanitize-recover=all", str(src), "-o", str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-500:]
+    most = (1 << 24) - 1
+    want = [0, 0, 0, 1, 1, 1, 1, most, most - (1 << 17), most]
+    assert [int(x) for x in r.stdout.split()] == [x << 8 | 250 for x in want]
