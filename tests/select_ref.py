@@ -163,3 +163,21 @@ def backward_sure(logits, ids, dw, score, renorm, scale, dscores=None):
         out.append(dl)
         bound.append([x + 1e-37 for x in err])
     return torch.tensor(out, dtype=torch.float64).view(T, E), torch.tensor(bound, dtype=torch.float64).view(T, E)
+
+
+def gradient_chain(y, dout, pos, dw, logits, ids, dl, dscores, score, renorm=True, scale=1.0):
+    """A run's gradients of the weights and of the logits, each from what the step before it wrote: the largest error of
+    dw [T, k] over its bound, of dl [T, E] (fp32) over its bound, and the norm of dl's bound over that of the part of dl
+    that comes through the weights (what the second ratio can tell of it).
+
+    dw: dout . y of the slot's row (pos, -1 none) in 64 bits; H products, each off by half a step of fp32, and H sums by a
+    step of what they run over. dl: backward() of the dw that was written, with its bound, and dl's own rounding."""
+    H = y.shape[1]
+    rows = torch.where(pos[..., None] >= 0, y.double()[pos.long().clamp(min=0)], 0.0) * dout.double()[:, None]
+    err = (dw.double() - rows.sum(2)).abs()
+    first = (err / (2 * H * 2.0 ** -23 * rows.abs().sum(2) + 1e-37)).max().item()
+    want, bound = backward(logits, ids, dw, score, renorm, scale, dscores)
+    without, _ = backward(logits, ids, torch.zeros_like(dw), score, renorm, scale, dscores)
+    bound = bound + 2.0 ** -24 * (want.abs() + bound)
+    second = ((dl.double() - want).abs() / bound).max().item()
+    return first, second, (bound.norm() / (want - without).norm()).item()

@@ -255,3 +255,17 @@ def test_choice_of_moe_route():
     # both are softmaxes over the chosen logits; moe_route's in fp32: differences (far) 2^-24 of at most 16, an
     # exponential, a sum of six, a quotient
     assert bool(((w2 - w).abs() <= 40 * 2.0 ** -24 * w2).all())
+
+
+@pytest.mark.parametrize("route", [GROUPED, PLAIN, WHOLE])
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 4, 64, 64), (37, 3, 8, 128, 64), (150, 2, 4, 192, 128), (60, 4, 16, 320, 192)])
+def test_training_pass_logits_step_by_step(T, k, E, H, I, route):
+    """The weights' and the logits' gradients, each against 64 bits from what the step before it wrote, to fp32 roundings."""
+    L = layer(T + 5, T, k, E, H, I, **route)
+    b = buffers(L)
+    train(L, b)
+    c = {n: v.cpu() for n, v in dict(b, **{n: L[n] for n in ("dout", "logits", "dscores")}).items()}
+    kind = {n: v for n, v in route.items() if n in ("score", "renorm", "scale")}
+    dw, dl, share = select_ref.gradient_chain(c["y"], c["dout"], c["pp"].view(T, k), c["dw"], c["logits"], c["ids"], c["dl"],
+                                              c["dscores"], **kind)
+    assert dw <= 1 and dl <= 1 and share < 1e-3

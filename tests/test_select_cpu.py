@@ -165,3 +165,28 @@ int main() {
     most = (1 << 24) - 1
     want = [0, 0, 0, 1, 1, 1, 1, most, most - (1 << 17), most]
     assert [int(x) for x in r.stdout.split()] == [x << 8 | 250 for x in want]
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+def test_check_of_the_gradients_finds_mistakes(score, renorm):
+    """What the layer's test asks of a training pass, asked of right results and of each planted mistake."""
+    g = torch.Generator().manual_seed(3)
+    T, k, E, H = 12, 3, 8, 32
+    l, ds = torch.randn(T, E, generator=g), torch.randn(T, E, generator=g)
+    ids = ref.select(l, k, score)[0]
+    y, dout = torch.randn(T * k, H, generator=g), torch.randn(T, H, generator=g).bfloat16()
+    pos = torch.randperm(T * k, generator=g).view(T, k)
+    ids[2, 1], pos[2, 1] = -1, -1
+    rows = torch.where(pos[..., None] >= 0, y[pos.clamp(min=0)], 0.0)
+    dw = (rows.double() * dout.double()[:, None]).sum(2).float()
+    back = lambda d, r=renorm, sc=2.5: ref.backward(l, ids, d, score, r, sc, ds)[0].float()  # noqa: E731
+    def holds(dw, dl):
+        a, b, share = ref.gradient_chain(y, dout, pos, dw, l, ids, dl, ds, score, renorm, 2.5)
+        return a <= 1 and b <= 1 and share < 1e-3
+
+    assert holds(dw, back(dw))
+    wrong = [(dw, torch.zeros(T, E)), (dw, back(0 * dw)), (dw, back(dw.roll(1, 1))), (dw.roll(1, 1), back(dw.roll(1, 1))),
+             (dw.roll(1, 0), back(dw.roll(1, 0))), (dw, back(dw, sc=1.0)), (dw, back(dw, r=not renorm)), (dw, back(dw).roll(1, 1)),
+             (0 * dw, back(0 * dw)), (dw, back(dw * (1 + 2.0 ** -9)))]
+    for i, w in enumerate(wrong):
+        assert not holds(*w), i
