@@ -478,7 +478,9 @@ moe_status moe_w4_dequantize(const uint8_t* codes, int32_t scale_dtype, const vo
  * every product exact, in fp32 sums over each group, which join the result times their
  * scale (fixed order). A row with an infinity or a NaN has any such values in its
  * results; other rows stay below 2^113 in magnitude (a group's sum of z x has to stay
- * inside fp32); scales are finite, or NaN for columns of NaN. From one row per expert to
+ * inside fp32); scales are finite, or NaN for columns of NaN, and with zero points s z is
+ * inside fp32 (as for all scales below 2^120), since s sum q x and s z sum x join the result
+ * one by one, which both have to stay inside fp32, too. From one row per expert to
  * thousands; the input gradient through frozen weights is moe_w4_dequantize and
  * moe_grouped_gemm with w_trans 0. */
 moe_status moe_w4_grouped_gemm(const void* a, int64_t a_rows, const int32_t* row_index,

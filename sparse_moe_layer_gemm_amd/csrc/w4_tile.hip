@@ -24,7 +24,8 @@
 // 983, without the group sums 905, MFMAs alone 695); 1998 rows over 48 experts, 1440 x 2056,
 // G = 32 with zero points: 67 us on the small tile.
 // Scales s and zero points of the tile's columns are fetched 8 groups ahead, 16 bytes of a
-// column at a time; s and s z stand in LDS as fp32, groups apart.
+// column at a time; s and s z stand in LDS as fp32, groups apart (so s z has to stay inside fp32, which
+// include/moe.h asks for: held as s z / 256 against 256 t it would lose the last bits of scales below 2^-118).
 #include "w4_common.h"
 
 namespace moe {

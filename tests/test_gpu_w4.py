@@ -320,3 +320,23 @@ def test_streams_and_graphs():
         moe.moe_w4_grouped_gemm(xs[2], codes, s, off, eager, zeros=z)
         torch.cuda.synchronize()
         assert torch.equal(o, want[i]) and torch.equal(eager, want[2])
+
+
+@pytest.mark.parametrize("per,N", [(1, 136), (20, 136), (300, 136), (2500, 800)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("sdtype", [F32, BF])
+def test_largest_scales(per, N, group, sdtype):
+    """Scales just below 2^120 with zero points of 255, at which s z is just inside fp32: rows of zeros, and rows whose
+    sums over a group vanish, have finite results, the former zeros."""
+    g, E, K = gen(group), 2, 384
+    M = E * per
+    a = normal(g, M, K // 2) * 2.0 ** -20
+    a = torch.stack((a, -a), 2).flatten(1).to(BF)
+    a[::3] = 0
+    codes, s, z = weights(g, E, N, K, group, True, sdtype)
+    s.copy_(torch.sign(s.float()) * 2.0 ** 120 * (1 - 2.0 ** -8))
+    z[..., ::2] = 255
+    check_product(a, [per] * E, codes, s, z, F32, spare=0)
+    out = torch.empty(M, N, device="cuda")
+    moe.moe_w4_grouped_gemm(a, codes, s, ops_ref.offsets_of([per] * E), out, zeros=z)
+    assert out.isfinite().all() and not out[::3].any() and out[1::3].any() == (M > 1)
