@@ -269,9 +269,10 @@ hipError_t launch(const GroupedArgs& g, const W4& w, hipStream_t st) {
 //    64 x 32           336     290     216     187     (tiles 184)
 // So: two wavefronts where there are workgroups enough and the tables leave room for five or
 // more of them in a CU's LDS, else four; 16 rows where experts have more than four.
+bool wide_rows(const GroupedArgs& g) { return g.M > 4LL * (g.E < g.M ? g.E : g.M); }
 template <int G, bool SF32, bool Z>
 hipError_t launch_rows(const GroupedArgs& g, const W4& w, hipStream_t st) {
-  const bool wide = g.M > 4LL * (g.E < g.M ? g.E : g.M);
+  const bool wide = wide_rows(g);
   const bool many = groups_of(g, wide ? 16 : 8) > 512 && table_bytes(g, w) <= 16 * 1024;
   if (wide) return many ? launch<G, SF32, Z, 16, 2>(g, w, st) : launch<G, SF32, Z, 16, 4>(g, w, st);
   return many ? launch<G, SF32, Z, 8, 2>(g, w, st) : launch<G, SF32, Z, 8, 4>(g, w, st);
@@ -288,9 +289,14 @@ hipError_t launch_g(const GroupedArgs& g, const W4& w, hipStream_t st) {
 // against the faster tiles, by experts x rows: 1 x 16 14, 32; 1 x 128 28, 47; 1 x 256 41, 47; 1 x 512 70, 56;
 // 16 x 32 34, 48; 16 x 64 57, 60; 16 x 128 90, 62; 64 x 16 80, 97; 64 x 32 112, 106; 64 x 64 179, 143;
 // 256 x 16 276, 301; 256 x 32 405, 347; 48 x 42 at 1440 x 2056, G = 32: 94, 71. So: below 32 rows per expert, and
-// where the tiles are too few for the CUs; if the scales of 64 columns fit in LDS, and the grid in a launch.
+// where the tiles are too few for the CUs; if the grid fits in a launch, and the scales of 64 columns in LDS.
+// Scales of more than 64 KB leave room for one workgroup in a CU, and then two rounds of them are as many as pay. At
+// 14336 x 4096, G = 32 with zero points (86 KB): 1 x 1 52, 128; 1 x 64 55, 196; 8 x 1 108, 138; 8 x 8 111, 151;
+// 8 x 16 173, 165; 8 x 30 263, 203; 1 x 256 208, 199; 64 experts x 2 rows at 7168 x 2048 with fp32 scales (72 KB): 190, 177.
 bool w4_prefer_stream(const GroupedArgs& g, const W4& w) {
-  if (table_bytes(g, w) > 64 * 1024 || tile_grid(g, 8, (g.N + BN - 1) / BN) * 256 >= (1LL << 32)) return false;
+  const int rm = wide_rows(g) ? 16 : 8, tables = table_bytes(g, w);
+  if (4 * stage_bytes(rm) + tables > kLds || tile_grid(g, 8, (g.N + BN - 1) / BN) * 256 >= (1LL << 32)) return false;
+  if (tables > 64 * 1024 && groups_of(g, rm) > 512) return false;
   const long long e = g.E < g.M ? g.E : g.M;
   return g.M < 32 * e || e * ((g.M + 64 * e - 1) / (64 * e)) * ((g.N + 127) / 128) <= 192;
 }

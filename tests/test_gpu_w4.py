@@ -340,3 +340,14 @@ def test_largest_scales(per, N, group, sdtype):
     out = torch.empty(M, N, device="cuda")
     moe.moe_w4_grouped_gemm(a, codes, s, ops_ref.offsets_of([per] * E), out, zeros=z)
     assert out.isfinite().all() and not out[::3].any() and out[1::3].any() == (M > 1)
+
+
+@pytest.mark.parametrize("K", [7168, 14336, 16352, 16384, 19104, 19136])
+@pytest.mark.parametrize("counts,N", [([1], 136), ([0, 3, 4], 72), ([5, 9], 72), ([16, 0, 1], 264), ([64], 520), ([1] * 9, 4096)])
+@pytest.mark.parametrize("sdtype", [F32, BF])
+def test_scales_of_long_rows(K, counts, N, sdtype):
+    """Depths whose scales and zero points fill LDS beside the streaming form's stages, up to its end and past it."""
+    g = gen(K)
+    a = normal(g, sum(counts), K)
+    codes, s, z = weights(g, len(counts), N, K, 32, True, sdtype)
+    check_product(a, counts, codes, s, z, BF, spare=0)
