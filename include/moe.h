@@ -431,9 +431,9 @@ moe_status moe_mxfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scale
  * rounded once to dl_dtype (dlogits [T, E]). What the chosen ones' weights give them is formed
  * in fp64, what the other scores give in fp32, off as the scores are; sums run over differences
  * to the expert that has more than half of all scores (of the chosen ones'), if there is one, so
- * that the gradients of a token that is sure of its expert keep their digits. A slot whose id lies outside [0, E)
- * has no gradient, nor has an expert that is left out; an expert that two slots
- * name gets the sum. Limits as above. */
+ * that the gradients of a token that is sure of its expert keep their digits. A slot
+ * whose id lies outside [0, E) has no gradient, nor has an expert that is left out; an
+ * expert that two slots name gets the sum. Limits as above. */
 typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 moe_status moe_select(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k,
                       int32_t score, const float* bias, int32_t groups, int32_t group_k,

@@ -20,18 +20,23 @@
 //    the next are D (a logit's: 1) units apart.
 //  - 64-bit keys, as fp64 numbers (of which a maximum or minimum is one instruction, too):
 //    the logit, or score + bias formed in fp64 and kept to 44 bits. A wavefront takes
-//    them where one of its tokens is not certain, about one in a hundred, or whose largest
-//    choice a bias takes past 1000 in magnitude.
+//    them, on top of the others, where one of its tokens is not certain, or has a largest
+//    choice that a bias takes past 1000 in magnitude. How many do depends on the data: about one
+//    in a hundred for fp32 logits and biases that are independent numbers, most of them where
+//    choices are equal, since equal ones count as too close, though their ids order them. 131072
+//    tokens x 256 experts, 8 chosen, sigmoid (softmax), us: bf16 logits without a bias 44 (42); normal
+//    biases 75 (82), in steps of 0.001 75 (96), bf16 numbers near 8 113 (117), all zero 141 (133); fp32
+//    logits 44 (44), 73 (84), 73 (96), 75 (115), 79 (88).
 // Weights and scores are formed alike on both ways.
 //
 // Groups: the choices cross through LDS, slots left free after each group so that lanes that
 // walk neighbouring groups meet different banks; several lanes share a group while there
 // are 8 at most.
 //
-// Bound by vector instructions, about 1200 for four tokens of 160 experts with bias and
-// groups. Measured: 131072 tokens x 160 experts, 6 chosen from 3 of 8 groups with a bias,
-// all scores written: 80 us (2.2 TB/s; 107 with fp64 keys alone; without bias and groups 36);
-// 128 tokens x 256 experts, 8 from 4 of 8 groups: 7.0 us.
+// Bound by vector instructions, 1140 for four tokens of 160 experts with bias and
+// groups, 96 % of the SIMDs' cycles. Measured: 131072 tokens x 160 experts, 6 chosen from 3 of 8 groups with a bias,
+// all scores written: 81 us (2.2 TB/s; 107 with fp64 keys alone; without bias and groups 37);
+// 128 tokens x 256 experts, 8 from 4 of 8 groups: 7.1 us.
 #include "select_common.h"
 #include "select_internal.h"
 #include "select_keys.h"

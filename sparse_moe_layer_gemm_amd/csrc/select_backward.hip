@@ -17,8 +17,8 @@
 // that of the expert that has more than half, which leaves the sum to the others and takes
 // nothing from their digits. The parts of h, d and g, are moved each by itself.
 //
-// 16 lanes hold a token (select_common.h). C and D cross through LDS. Bound by HBM: 131072 tokens
-// x 256 experts with d scores 67 us, 4.1 TB/s.
+// 16 lanes hold a token (select_common.h). C and D cross through LDS. Bound by HBM and vector
+// instructions (79 % of the SIMDs' cycles): 131072 tokens x 256 experts with d scores 66 us, 4.2 TB/s.
 #include "select_common.h"
 #include "select_internal.h"
 

@@ -13,7 +13,7 @@
 // rounded to multiples of 2^-10 tells both apart, and is then rounded to a whole number.
 //
 // Bound by HBM: 32 x 5120 x 1536 transposed 131 us (4.9 TB/s), and back 86 us (7.3 TB/s, past
-// the caches); 1536 x 5120 by rows 7.4 us.
+// the caches); 1536 x 5120 by rows 7.2 us.
 #include "ops_common.h"
 #include "w4_internal.h"
 

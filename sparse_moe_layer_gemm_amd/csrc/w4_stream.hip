@@ -285,8 +285,9 @@ hipError_t launch_g(const GroupedArgs& g, const W4& w, hipStream_t st) {
 
 }  // namespace
 
-// The streaming kernel or tiles? Measured at 5120 x 1536 (one expert: 5120 x 5120), G = 128, us, streaming
-// against the faster tiles, by experts x rows: 1 x 16 14, 32; 1 x 128 28, 47; 1 x 256 41, 47; 1 x 512 70, 56;
+// The streaming kernel or tiles? By the average load, which is what the host knows: an expert far above it streams its
+// rows 16 at a time and turns its codes into bf16 as often. Measured with nearly even loads at 5120 x 1536 (one
+// expert: 5120 x 5120), G = 128, us, streaming against the faster tiles, by experts x rows: 1 x 16 14, 32; 1 x 128 28, 47; 1 x 256 41, 47; 1 x 512 70, 56;
 // 16 x 32 34, 48; 16 x 64 57, 60; 16 x 128 90, 62; 64 x 16 80, 97; 64 x 32 112, 106; 64 x 64 179, 143;
 // 256 x 16 276, 301; 256 x 32 405, 347; 48 x 42 at 1440 x 2056, G = 32: 94, 71. So: below 32 rows per expert, and
 // where the tiles are too few for the CUs; if the grid fits in a launch, and the scales of 64 columns in LDS.

@@ -18,11 +18,13 @@
 // The depth is walked in whole stages: behind its end rows are zeros, codes anything
 // finite, and scales 0.
 //
-// Bound by the issue of instructions: per 256 of depth a wavefront of the large tile has 637
-// vector instructions (2550 cycles) beside 136 MFMAs (2180 cycles), and they hardly overlap.
-// 32768 rows over 64 experts, 5120 x 2560, G = 128: 1016 us, 846 TFLOP/s (without its loads
-// 983, without the group sums 905, MFMAs alone 695); 1998 rows over 48 experts, 1440 x 2056,
-// G = 32 with zero points: 67 us on the small tile.
+// Bound by the issue of instructions: per 256 of depth a wavefront of the large tile has 676
+// vector instructions (2700 cycles: 288 turn codes into bf16, 128 add the groups' sums, 128 take the zero
+// points away, the rest are addresses, selects and compares) beside 136 MFMAs (2180 cycles). By the
+// counters the SIMDs spend 54 % of their cycles on the former and 41 % on the latter: next to no time is free, and
+// next to none overlaps. 32768 rows over 64 experts, 5120 x 2560, G = 128: 1016 us, 846 TFLOP/s (without its
+// loads 983, without the group sums 905, MFMAs alone 695); 1998 rows over 48 experts, 1440 x 2056,
+// G = 32 with zero points: 66 us on the small tile (vector instructions 51 %, MFMAs 15 %).
 // Scales s and zero points of the tile's columns are fetched 8 groups ahead, 16 bytes of a
 // column at a time; s and s z stand in LDS as fp32, groups apart (so s z has to stay inside fp32, which
 // include/moe.h asks for: held as s z / 256 against 256 t it would lose the last bits of scales below 2^-118).
@@ -461,7 +463,8 @@ long long tiles_of(const GroupedArgs& g, int bm, int bn) {
   const long long e = g.E < g.M ? g.E : g.M;
   return e * ((g.M + bm * e - 1) / (bm * e)) * ((g.N + bn - 1) / bn);
 }
-// Which tile? 512 small ones take 0.56 of 256 large ones' time where both fill the CUs, so the
+// Which tile? It goes by the average load, as all rules here do, and so were they measured: no host call
+// knows the loads themselves. 512 small ones take 0.56 of 256 large ones' time where both fill the CUs, so the
 // shape with fewer rounds at those weights. Measured at 5120 x 1536, G = 128, us, large against
 // small, experts x rows: 64 x 64 180, 143; 64 x 128 265, 216; 64 x 256 356, 372; 64 x 512 620, 698;
 // 256 x 128 822, 810; 16 x 128 92, 62; one expert, 5120 x 5120: 512 rows 87, 56; 1024 rows 88, 89;
