@@ -256,6 +256,9 @@ hipError_t launch(const GroupedArgs& g, const W4& w, hipStream_t st) {
   w4_stream_kernel<G, SF32, Z, RM, WV><<<(unsigned)n, 64 * WV, tables, st>>>(g, w, nt);
   return hipGetLastError();
 }
+// 16 rows per tile rather than 8?
+bool wide_rows(const GroupedArgs& g) { return g.M > 4LL * (g.E < g.M ? g.E : g.M); }
+
 // Rows per tile and wavefronts per workgroup. Measured at 5120 x 1536, G = 128, with weights
 // that no cache holds, us (8 x 4: 8 rows, 4 wavefronts):
 //   experts x rows   8 x 4   8 x 2   16 x 4   16 x 2
@@ -269,7 +272,6 @@ hipError_t launch(const GroupedArgs& g, const W4& w, hipStream_t st) {
 //    64 x 32           336     290     216     187     (tiles 184)
 // So: two wavefronts where there are workgroups enough and the tables leave room for five or
 // more of them in a CU's LDS, else four; 16 rows where experts have more than four.
-bool wide_rows(const GroupedArgs& g) { return g.M > 4LL * (g.E < g.M ? g.E : g.M); }
 template <int G, bool SF32, bool Z>
 hipError_t launch_rows(const GroupedArgs& g, const W4& w, hipStream_t st) {
   const bool wide = wide_rows(g);
@@ -287,8 +289,8 @@ hipError_t launch_g(const GroupedArgs& g, const W4& w, hipStream_t st) {
 
 // The streaming kernel or tiles? By the average load, which is what the host knows: an expert far above it streams its
 // rows 16 at a time and turns its codes into bf16 as often. Measured with nearly even loads at 5120 x 1536 (one
-// expert: 5120 x 5120), G = 128, us, streaming against the faster tiles, by experts x rows: 1 x 16 14, 32; 1 x 128 28, 47; 1 x 256 41, 47; 1 x 512 70, 56;
-// 16 x 32 34, 48; 16 x 64 57, 60; 16 x 128 90, 62; 64 x 16 80, 97; 64 x 32 112, 106; 64 x 64 179, 143;
+// expert: 5120 x 5120), G = 128, us, streaming against the faster tiles, by experts x rows:
+// 1 x 16 14, 32; 1 x 128 28, 47; 1 x 256 41, 47; 1 x 512 70, 56; 16 x 32 34, 48; 16 x 64 57, 60; 16 x 128 90, 62; 64 x 16 80, 97; 64 x 32 112, 106; 64 x 64 179, 143;
 // 256 x 16 276, 301; 256 x 32 405, 347; 48 x 42 at 1440 x 2056, G = 32: 94, 71. So: below 32 rows per expert, and
 // where the tiles are too few for the CUs; if the grid fits in a launch, and the scales of 64 columns in LDS.
 // Scales of more than 64 KB leave room for one workgroup in a CU, and then two rounds of them are as many as pay. At

@@ -342,11 +342,12 @@ def test_largest_scales(per, N, group, sdtype):
     assert out.isfinite().all() and not out[::3].any() and out[1::3].any() == (M > 1)
 
 
-@pytest.mark.parametrize("K", [7168, 14336, 16352, 16384, 19104, 19136])
+@pytest.mark.parametrize("K", [7168, 9728, 9760, 11392, 11424, 14336, 16256, 16288, 18944, 18976])
 @pytest.mark.parametrize("counts,N", [([1], 136), ([0, 3, 4], 72), ([5, 9], 72), ([16, 0, 1], 264), ([64], 520), ([1] * 9, 4096)])
 @pytest.mark.parametrize("sdtype", [F32, BF])
 def test_scales_of_long_rows(K, counts, N, sdtype):
-    """Depths whose scales and zero points fill LDS beside the streaming form's stages, up to its end and past it."""
+    """Depths whose scales and zero points fill LDS beside the streaming form's stages. The last that fit, and the next:
+    fp32 scales 9728 with 16 rows to a tile, 11392 with 8; bf16 ones 16256 and 18944."""
     g = gen(K)
     a = normal(g, sum(counts), K)
     codes, s, z = weights(g, len(counts), N, K, 32, True, sdtype)
